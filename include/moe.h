@@ -328,6 +328,137 @@ moe_status moe_forward_noalloc(const moe_layer* L, const float* logits, const fl
                                uint32_t route_flags, uint32_t ffn_flags, const moe_routing* r, float* y_pair,
                                float* y_shared, const float* shared_scale, float* out, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Scored routing: softmax or sigmoid scores, a balance bias, expert groups.
+ * ------------------------------------------------------------------------ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+/* How a layer turns router logits l into experts and weights:
+ *   s = softmax(l) over the E logits, or 1 / (1 + exp(-l)) of each;
+ *   c = s + bias (bias NULL: c = s);
+ *   with n_group > 1 the experts form n_group groups of E/n_group consecutive
+ *   ones; a group's score is the sum of its group_top (1 or 2) largest c, and
+ *   only the topk_group groups with the largest scores stay (ties to the lower
+ *   group);
+ *   of what stays, the k experts with the largest c, in descending order, ties
+ *   to the lower index;
+ *   w = s at the selected experts (without the bias), divided by their sum
+ *   when renorm != 0 (a sum of 0 gives weights 0), times scale.
+ * s, c and the sums are fp64, each weight is rounded once to fp32. */
+typedef struct moe_route_spec {
+    int32_t score;      /* MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID */
+    int32_t n_group;    /* 1: no groups; else a divisor of E, at most 64 */
+    int32_t topk_group; /* 1..n_group, with k <= topk_group * E/n_group */
+    int32_t group_top;  /* 1 or 2, at most E/n_group */
+    int32_t renorm;
+    float scale;        /* finite */
+    const float* bias;  /* fp32 [E] on the device, or NULL; -inf bars an expert from
+                           selection while k others are left */
+} moe_route_spec;
+
+/* Expert selection by a score rule, plus the per-expert bucketing of
+ * moe_route_topk: same routing buffers, same workspace
+ * (moe_route_workspace_bytes), same limits on T, E and k.  A NaN or infinite
+ * logit, and a bias that is NaN or +inf, set the device error word (that
+ * token's slots still hold k distinct experts). */
+moe_status moe_route_scored(const float* logits, int32_t T, int32_t E, int32_t k, const moe_route_spec* spec,
+                            const moe_routing* r, void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit float weights and activations: OCP e4m3 codes, fp32 scales.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of activations and outputs, numbered as in GGUF. */
+enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 30 };
+
+#define MOE_FP8_BLOCK 128
+
+/* n_experts matrices of rows x cols e4m3 codes (one byte each, cols
+ * contiguous, rows row_stride bytes and experts expert_stride bytes apart), one
+ * fp32 scale per 128 x 128 block: scale [n_experts][ceil(rows/128)][ceil(cols/128)],
+ * contiguous; w = scale * code.  cols a multiple of 16; data, row_stride and
+ * expert_stride multiples of 16 bytes; scale 4-byte aligned. */
+typedef struct moe_fp8_matrix {
+    const void* data;
+    const float* scale;
+    int32_t rows;
+    int32_t cols;
+    int64_t row_stride;
+    int64_t expert_stride;
+} moe_fp8_matrix;
+
+/* One MoE layer over e4m3 experts: gate/up [E][I][H], down [E][H][I]; with
+ * has_shared != 0 the sh_* matrices hold the always-on shared expert. */
+typedef struct moe_fp8_layer {
+    int32_t n_experts; /* E, at most 1024 */
+    int32_t hidden;    /* H, a multiple of 128, at most 16384 */
+    int32_t inter;     /* I, a multiple of 128, at most 16384 */
+    int32_t has_shared;
+    moe_fp8_matrix gate, up, down;
+    moe_fp8_matrix sh_gate, sh_up, sh_down;
+} moe_fp8_layer;
+
+/* Activation quantisation, once per row and 128 columns: a = max|x| of the
+ * block; a == 0 gives codes and scale 0; otherwise q = e4m3(x * 448 / a),
+ * rounded to nearest, ties to even, and d = a / 448 (correctly rounded).  For
+ * F16 and BF16 inputs the codes are those of exact arithmetic; for F32 ones
+ * x * 448 / a carries an fp32 rounding.  A block with 0 < a < 2^-116 is
+ * quantised as if a were 2^-116.
+ * x [T][H] of x_type, rows ldx elements apart -> xq [T][H] (contiguous), xs
+ * fp32 [T][ceil(H/128)].  Checks: T >= 1; H a positive multiple of 16; ldx >= H;
+ * x and every row of it 16-byte aligned; xq 8-byte aligned, xs 4-byte.  A
+ * non-finite x sets the device error word and its block is written as codes 0,
+ * scale 0. */
+moe_status moe_quantize_fp8(const void* x, int32_t x_type, int64_t ldx, int32_t T, int32_t H, void* xq, float* xs,
+                            hipStream_t stream);
+
+/* Dense block-scaled product:
+ *   y[t][n] = sum_b xs[t][b] * ws[n/128][b] * sum_{j in block b} xq[t][j] * wq[n][j]
+ * xq [T][K] and xs [T][ceil(K/128)] from moe_quantize_fp8 (K = w->cols), w one
+ * matrix (N = w->rows); y [T][N] of y_type, rows ldy elements apart.  The sum
+ * over b is fp32, y is rounded once.  For an fp32 y the block products are
+ * summed in fp32 too; for bf16 and fp16 the 8-bit matrix unit forms them, which
+ * drops bits below 2^-13 of the largest of each eight consecutive products
+ * (their sum is off by at most 7 * 2^-13 of it).  A row of y depends
+ * on its own row of xq and xs only, but the order of its fp32 sum follows
+ * from T (as moe_router_logits).  Checks: T >= 1; K a positive multiple of 16;
+ * N >= 1; ldy >= N; xq 16-byte aligned; y aligned to its type. */
+moe_status moe_matmul_fp8(const void* xq, const float* xs, int32_t T, const moe_fp8_matrix* w, void* y,
+                          int32_t y_type, int64_t ldy, hipStream_t stream);
+
+/* Bytes of device workspace moe_expert_ffn_fp8 needs. */
+size_t moe_ffn_fp8_workspace_bytes(const moe_fp8_layer* L, int32_t T, int32_t k);
+
+/* Expert FFN for every routed (token, slot) pair, and for the shared expert:
+ *   y_pair[p] = W_down[e] * q(silu(W_gate[e] x_t) .* (W_up[e] x_t)),  e = idx[p], t = p / k
+ * with q the quantisation of moe_quantize_fp8 per (pair, 128 columns of I) and
+ * every product as in moe_matmul_fp8 with an fp32 y.  xq, xs from moe_quantize_fp8; y_pair fp32
+ * [T*k][H]; y_shared fp32 [T][H] (required iff has_shared); both 16-byte
+ * aligned.  r as in moe_expert_ffn_q, from moe_route_topk or moe_route_scored
+ * for the same T, k and E.  Workspace 256-byte aligned. */
+moe_status moe_expert_ffn_fp8(const moe_fp8_layer* L, const moe_routing* r, int32_t T, int32_t k, const void* xq,
+                              const float* xs, float* y_pair, float* y_shared, void* workspace, size_t ws_bytes,
+                              hipStream_t stream);
+
+/* Bytes of device workspace moe_forward_fp8 needs. */
+size_t moe_forward_fp8_workspace_bytes(const moe_fp8_layer* L, int32_t T, int32_t k, uint32_t ffn_flags);
+
+/* The whole layer over e4m3 experts: routing (as moe_route_scored, results
+ * written to r), quantisation of x (as moe_quantize_fp8), expert FFN (as
+ * moe_expert_ffn_fp8) and
+ *   out[t] = sum_j w[t][j] * y_pair[t*k+j]  (+ s_t * y_shared[t])
+ * summed in fp32 in slot order and rounded once to x's type; with bf16 x the
+ * products are those of moe_matmul_fp8 with a bf16 y, else with an fp32 y.  s_t =
+ * shared_scale[t], or 1 when NULL (non-NULL needs a shared expert).  x and out
+ * [T][H] of x_type, contiguous and 16-byte aligned; out may be x.  The per-pair
+ * and shared outputs stay in the workspace: as fp32, or with ffn_flags =
+ * MOE_FFN_PAIR_BF16 as bf16 (out then moves by at most 2^-8 * (sum_j |w_j*y_j| +
+ * |s_t*y_shared|) per element); ffn_flags is otherwise 0. */
+moe_status moe_forward_fp8(const moe_fp8_layer* L, const moe_route_spec* spec, const float* logits, const void* x,
+                           int32_t x_type, int32_t T, int32_t k, uint32_t ffn_flags, const moe_routing* r,
+                           const float* shared_scale, void* out, void* workspace, size_t ws_bytes,
+                           hipStream_t stream);
+
 /* Test hook: dequantize n_weights weights of contiguous blocks to fp32 with the
  * unpacking helpers of the general (unfused) kernels.  Each value is the exact
  * d*sc*q - dmin*m (Q4_K, Q5_K), d*q (Q8_0) or d*q + m (Q5_1) rounded once to

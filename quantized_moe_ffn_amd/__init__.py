@@ -11,7 +11,10 @@ Entry points keep the C names: ``moe_route_topk``, ``moe_quantize_act``,
 ``moe_forward``, ``moe_forward_ep``, ``moe_forward_noalloc``, ``moe_forward_router``, ``moe_dequant_q``,
 ``moe_check_device_errors``, ``moe_last_error``, ``moe_abi_version``,
 ``moe_route_workspace_bytes``, ``moe_ffn_workspace_bytes``,
-``moe_forward_workspace_bytes``.
+``moe_forward_workspace_bytes``; and for routing by a score rule and experts in
+8-bit floats ``moe_route_scored``, ``moe_quantize_fp8``, ``moe_matmul_fp8``,
+``moe_expert_ffn_fp8``, ``moe_forward_fp8``, ``moe_ffn_fp8_workspace_bytes``,
+``moe_forward_fp8_workspace_bytes``.
 """
 from __future__ import annotations
 
@@ -33,6 +36,13 @@ MOE_FFN_DECODE = 1
 MOE_FFN_INT8 = 2
 MOE_FFN_PAIR_BF16 = 16  # layer calls: per-pair outputs stay in the workspace (bf16 on the MFMA GEMMs)
 
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_F32 = 0
+MOE_F16 = 1
+MOE_BF16 = 30
+MOE_FP8_BLOCK = 128
+
 BLOCK_WEIGHTS = {MOE_Q4_K: 256, MOE_Q5_K: 256, MOE_Q8_0: 32, MOE_Q5_1: 32}
 BLOCK_BYTES = {MOE_Q4_K: 144, MOE_Q5_K: 176, MOE_Q8_0: 34, MOE_Q5_1: 24}
 
@@ -42,6 +52,8 @@ EXPORTS = (
     "moe_dequant_q", "moe_check_device_errors", "moe_forward_workspace_bytes", "moe_forward",
     "moe_router_logits", "moe_combine_ep", "moe_shared_gate", "moe_forward_ep", "moe_forward_noalloc",
     "moe_forward_router",
+    "moe_route_scored", "moe_quantize_fp8", "moe_matmul_fp8", "moe_ffn_fp8_workspace_bytes", "moe_expert_ffn_fp8",
+    "moe_forward_fp8_workspace_bytes", "moe_forward_fp8",
 )
 
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20   # the static workspace of moe_forward_noalloc, per GPU
@@ -72,6 +84,24 @@ class moe_epilogue(ctypes.Structure):
 
 class moe_routing(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("idx", "w", "count", "offset", "pair", "active", "n_active")]
+
+
+class moe_route_spec(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("bias", ctypes.c_void_p)]
+
+
+class moe_fp8_matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32), ("row_stride", ctypes.c_int64), ("expert_stride", ctypes.c_int64)]
+
+
+class moe_fp8_layer(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("hidden", ctypes.c_int32), ("inter", ctypes.c_int32),
+                ("has_shared", ctypes.c_int32), ("gate", moe_fp8_matrix), ("up", moe_fp8_matrix),
+                ("down", moe_fp8_matrix), ("sh_gate", moe_fp8_matrix), ("sh_up", moe_fp8_matrix),
+                ("sh_down", moe_fp8_matrix)]
 
 
 _lib = None
@@ -125,6 +155,23 @@ def load_library(path: str = LIB_PATH):
     lib.moe_combine_ep.restype = st
     lib.moe_shared_gate.argtypes = [P, i32, i32, P, P, P]
     lib.moe_shared_gate.restype = st
+    lib.moe_route_scored.argtypes = [P, i32, i32, i32, ctypes.POINTER(moe_route_spec), ctypes.POINTER(moe_routing), P,
+                                     sz, P]
+    lib.moe_route_scored.restype = st
+    lib.moe_quantize_fp8.argtypes = [P, i32, i64, i32, i32, P, P, P]
+    lib.moe_quantize_fp8.restype = st
+    lib.moe_matmul_fp8.argtypes = [P, P, i32, ctypes.POINTER(moe_fp8_matrix), P, i32, i64, P]
+    lib.moe_matmul_fp8.restype = st
+    lib.moe_ffn_fp8_workspace_bytes.argtypes = [ctypes.POINTER(moe_fp8_layer), i32, i32]
+    lib.moe_ffn_fp8_workspace_bytes.restype = sz
+    lib.moe_expert_ffn_fp8.argtypes = [ctypes.POINTER(moe_fp8_layer), ctypes.POINTER(moe_routing), i32, i32, P, P, P,
+                                       P, P, sz, P]
+    lib.moe_expert_ffn_fp8.restype = st
+    lib.moe_forward_fp8_workspace_bytes.argtypes = [ctypes.POINTER(moe_fp8_layer), i32, i32, u32]
+    lib.moe_forward_fp8_workspace_bytes.restype = sz
+    lib.moe_forward_fp8.argtypes = [ctypes.POINTER(moe_fp8_layer), ctypes.POINTER(moe_route_spec), P, P, i32, i32, i32,
+                                    u32, ctypes.POINTER(moe_routing), P, P, P, sz, P]
+    lib.moe_forward_fp8.restype = st
     lib.moe_check_device_errors.argtypes = [P]
     lib.moe_check_device_errors.restype = st
     _lib = lib
@@ -336,6 +383,228 @@ def moe_forward_router(layer: Layer, x, w_router, logits, k: int, routing: Routi
 
 def moe_check_device_errors(stream=None):
     _check(load_library().moe_check_device_errors(_stream(stream)), "moe_check_device_errors")
+
+
+# ----------------------------------------------------------------------------- scored routing, 8-bit floats
+
+_elem_ids = None
+
+
+def _elem_id(t) -> int:
+    """MOE_F32 / MOE_F16 / MOE_BF16 of a tensor (raises ValueError for another type)."""
+    global _elem_ids
+    if _elem_ids is None:
+        import torch
+        _elem_ids = {torch.float32: MOE_F32, torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
+    i = _elem_ids.get(t.dtype)
+    if i is None:
+        raise ValueError("dtype %s: supported are float32, float16 and bfloat16" % t.dtype)
+    return i
+
+
+def _need(name: str, t, itemsize: int, shape, device=None, integer: bool | None = None):
+    """Checks a tensor argument: element size, shape, contiguity and device."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.element_size() != itemsize or t.is_complex() or (integer is not None and t.is_floating_point() == integer):
+        raise ValueError("%s has dtype %s" % (name, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+
+
+def _fp8_codes(name: str, t):
+    import torch
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError("%s has dtype %s: e4m3 codes are float8_e4m3fn or uint8" % (name, t.dtype))
+
+
+def _launch_stream(device, stream) -> int:
+    """The stream of a call on tensors of `device`, which has to be the current one."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a GPU, got %s" % device)
+    if device.index != torch.cuda.current_device():
+        raise ValueError("tensors are on %s, the current device is cuda:%d" % (device, torch.cuda.current_device()))
+    return _stream(stream)
+
+
+class RouteSpec:
+    """Score rule of moe_route_scored: score "softmax" or "sigmoid", n_group groups of which
+    topk_group stay (group score: the sum of the group_top largest biased scores), renormalised
+    weights times scale; bias fp32 [E] on the device, or None."""
+
+    def __init__(self, score: str = "softmax", n_group: int = 1, topk_group: int = 1, group_top: int = 1,
+                 renorm: bool = True, scale: float = 1.0, bias=None):
+        if score not in ("softmax", "sigmoid"):
+            raise ValueError("score = %r: use 'softmax' or 'sigmoid'" % (score,))
+        if bias is not None:
+            _need("bias", bias, 4, (bias.numel(),), integer=False)
+        self.bias = bias
+        self._s = moe_route_spec(MOE_SCORE_SIGMOID if score == "sigmoid" else MOE_SCORE_SOFTMAX, n_group, topk_group,
+                                 group_top, 1 if renorm else 0, scale, _ptr(bias))
+
+    def struct(self) -> moe_route_spec:
+        return self._s
+
+    def check(self, E: int, device):
+        if self.bias is not None and (self.bias.numel() != E or self.bias.device != device):
+            raise ValueError("bias has %d entries on %s, expected %d on %s"
+                             % (self.bias.numel(), self.bias.device, E, device))
+
+
+class Fp8Matrix:
+    """A device bank of e4m3 matrices: codes [n][rows][cols] (float8_e4m3fn or uint8, columns contiguous,
+    rows and experts at any 16-byte multiple) and scales fp32 [n][ceil(rows/128)][ceil(cols/128)]."""
+
+    def __init__(self, data, scale):
+        _fp8_codes("data", data)
+        if data.dim() != 3:
+            raise ValueError("data has shape %s, expected [n][rows][cols]" % (tuple(data.shape),))
+        n, rows, cols = data.shape
+        if cols > 1 and data.stride(2) != 1:
+            raise ValueError("data: columns must be contiguous")
+        b = MOE_FP8_BLOCK
+        _need("scale", scale, 4, (n, (rows + b - 1) // b, (cols + b - 1) // b), data.device, integer=False)
+        self.data, self.scale, self.n, self.rows, self.cols = data, scale, n, rows, cols
+        self._s = moe_fp8_matrix(data.data_ptr(), scale.data_ptr(), rows, cols,
+                                 data.stride(1) if rows > 1 else (cols + 15) // 16 * 16,
+                                 data.stride(0) if n > 1 else (rows * max(cols, data.stride(1)) + 15) // 16 * 16)
+
+    def struct(self) -> moe_fp8_matrix:
+        return self._s
+
+
+class Fp8Layer:
+    """One MoE layer over e4m3 experts: gate/up [E][I][H], down [E][H][I], optional shared expert
+    (three one-expert matrices)."""
+
+    def __init__(self, gate: Fp8Matrix, up: Fp8Matrix, down: Fp8Matrix, shared=None):
+        mats = (gate, up, down) + (tuple(shared) if shared is not None else ())
+        if len(mats) not in (3, 6):
+            raise ValueError("shared: expected (gate, up, down)")
+        self.gate, self.up, self.down, self.shared = gate, up, down, shared
+        self.n_experts, self.inter, self.hidden = gate.n, gate.rows, gate.cols
+        self.device = gate.data.device
+        for m, n in zip(mats, (self.n_experts,) * 3 + (1,) * 3):
+            if m.n != n or m.data.device != self.device:
+                raise ValueError("a matrix bank holds %d experts on %s, expected %d on %s"
+                                 % (m.n, m.data.device, n, self.device))
+        s = moe_fp8_layer()
+        s.n_experts, s.hidden, s.inter = self.n_experts, self.hidden, self.inter
+        s.gate, s.up, s.down = gate.struct(), up.struct(), down.struct()
+        if shared is not None:
+            s.has_shared = 1
+            s.sh_gate, s.sh_up, s.sh_down = (m.struct() for m in shared)
+        self._s = s
+
+    def struct(self) -> moe_fp8_layer:
+        return self._s
+
+
+def _check_routing(routing: Routing, T: int, E: int, k: int, device):
+    if (routing.T, routing.E, routing.k) != (T, E, k) or routing.idx.device != device:
+        raise ValueError("routing buffers are for T, E, k = %d, %d, %d on %s, expected %d, %d, %d on %s"
+                         % (routing.T, routing.E, routing.k, routing.idx.device, T, E, k, device))
+
+
+def _ws(workspace, device):
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("workspace must be contiguous and on %s" % device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def moe_route_scored(logits, k: int, routing: Routing, spec: RouteSpec, workspace=None, stream=None):
+    """Expert selection by a score rule, with moe_route_topk's buffers and workspace (fp32 logits [T][E])."""
+    T, E = logits.shape
+    _need("logits", logits, 4, (T, E), integer=False)
+    _check_routing(routing, T, E, k, logits.device)
+    spec.check(E, logits.device)
+    wp, wn = _ws(workspace, logits.device)
+    st = load_library().moe_route_scored(logits.data_ptr(), T, E, k, ctypes.byref(spec.struct()),
+                                         ctypes.byref(routing.struct()), wp, wn, _launch_stream(logits.device, stream))
+    _check(st, "moe_route_scored")
+
+
+def moe_quantize_fp8(x, xq, xs, stream=None):
+    """x [T][H] (float32, float16 or bfloat16; columns contiguous, rows at any 16-byte multiple) to e4m3
+    codes xq [T][H] and scales xs fp32 [T][ceil(H/128)]."""
+    T, H = x.shape
+    if x.stride(1) != 1 and H > 1:
+        raise ValueError("x: columns must be contiguous")
+    _fp8_codes("xq", xq)
+    _need("xq", xq, 1, (T, H), x.device)
+    _need("xs", xs, 4, (T, (H + MOE_FP8_BLOCK - 1) // MOE_FP8_BLOCK), x.device, integer=False)
+    _check(load_library().moe_quantize_fp8(x.data_ptr(), _elem_id(x), x.stride(0) if T > 1 else H, T, H,
+                                           xq.data_ptr(), xs.data_ptr(), _launch_stream(x.device, stream)),
+           "moe_quantize_fp8")
+
+
+def moe_matmul_fp8(xq, xs, w: Fp8Matrix, y, stream=None):
+    """y [T][N] = block-scaled product of xq [T][K], xs (from moe_quantize_fp8) with one matrix [1][N][K];
+    y float32, float16 or bfloat16, columns contiguous, rows at any distance."""
+    T, K = xq.shape
+    _fp8_codes("xq", xq)
+    _need("xq", xq, 1, (T, w.cols), w.data.device)
+    _need("xs", xs, 4, (T, w.scale.shape[2]), w.data.device, integer=False)
+    if w.n != 1:
+        raise ValueError("w holds %d matrices, expected one" % w.n)
+    if tuple(y.shape) != (T, w.rows) or (y.stride(1) != 1 and w.rows > 1) or y.device != w.data.device:
+        raise ValueError("y has shape %s, strides %s on %s: expected %s, contiguous columns, on %s"
+                         % (tuple(y.shape), y.stride(), y.device, (T, w.rows), w.data.device))
+    _check(load_library().moe_matmul_fp8(xq.data_ptr(), xs.data_ptr(), T, ctypes.byref(w.struct()), y.data_ptr(),
+                                         _elem_id(y), y.stride(0) if T > 1 else w.rows,
+                                         _launch_stream(y.device, stream)), "moe_matmul_fp8")
+
+
+def moe_ffn_fp8_workspace_bytes(layer: Fp8Layer, T: int, k: int) -> int:
+    return int(load_library().moe_ffn_fp8_workspace_bytes(ctypes.byref(layer.struct()), T, k))
+
+
+def moe_expert_ffn_fp8(layer: Fp8Layer, routing: Routing, T: int, k: int, y_pair, xq, xs, y_shared=None,
+                       workspace=None, stream=None):
+    H, d = layer.hidden, layer.device
+    _check_routing(routing, T, layer.n_experts, k, d)
+    _fp8_codes("xq", xq)
+    _need("xq", xq, 1, (T, H), d)
+    _need("xs", xs, 4, (T, H // MOE_FP8_BLOCK), d, integer=False)
+    _need("y_pair", y_pair, 4, (T * k, H), d, integer=False)
+    if y_shared is not None:
+        _need("y_shared", y_shared, 4, (T, H), d, integer=False)
+    wp, wn = _ws(workspace, d)
+    st = load_library().moe_expert_ffn_fp8(ctypes.byref(layer.struct()), ctypes.byref(routing.struct()), T, k,
+                                           xq.data_ptr(), xs.data_ptr(), y_pair.data_ptr(), _ptr(y_shared), wp, wn,
+                                           _launch_stream(d, stream))
+    _check(st, "moe_expert_ffn_fp8")
+
+
+def moe_forward_fp8_workspace_bytes(layer: Fp8Layer, T: int, k: int, flags: int = 0) -> int:
+    return int(load_library().moe_forward_fp8_workspace_bytes(ctypes.byref(layer.struct()), T, k, flags))
+
+
+def moe_forward_fp8(layer: Fp8Layer, logits, x, k: int, routing: Routing, spec: RouteSpec, out, shared_scale=None,
+                    flags: int = 0, workspace=None, stream=None):
+    """The whole layer over e4m3 experts from fp32 logits [T][E] and x [T][H] (out has x's type; it may be x)."""
+    T, E = logits.shape
+    d = layer.device
+    _need("logits", logits, 4, (T, layer.n_experts), d, integer=False)
+    xt = _elem_id(x)
+    _need("x", x, x.element_size(), (T, layer.hidden), d)
+    _need("out", out, x.element_size(), (T, layer.hidden), d)
+    if out.dtype != x.dtype:
+        raise ValueError("out has dtype %s, expected x's %s" % (out.dtype, x.dtype))
+    if shared_scale is not None:
+        _need("shared_scale", shared_scale, 4, (T,), d, integer=False)
+    _check_routing(routing, T, E, k, d)
+    spec.check(E, d)
+    wp, wn = _ws(workspace, d)
+    st = load_library().moe_forward_fp8(ctypes.byref(layer.struct()), ctypes.byref(spec.struct()), logits.data_ptr(),
+                                        x.data_ptr(), xt, T, k, flags, ctypes.byref(routing.struct()),
+                                        _ptr(shared_scale), out.data_ptr(), wp, wn, _launch_stream(d, stream))
+    _check(st, "moe_forward_fp8")
 
 
 # ----------------------------------------------------------------------------- whole layer

@@ -31,7 +31,7 @@ def sources():
 
 def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, *FLAGS, os.path.join(CSRC, "libmoe.hip"), "-o", tmp]
+    cmd = [HIPCC, *FLAGS, os.path.join(CSRC, "lib.hip"), "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)

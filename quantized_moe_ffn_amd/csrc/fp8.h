@@ -1,0 +1,128 @@
+// fp8.h — internal launchers and device helpers of the scored routing and the
+// 8-bit float (OCP e4m3) path: quantiser, block-scaled products, expert layer.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+
+// ------------------------------------------------------------------ scored routing
+
+struct ScoreRule {
+    int sigmoid;        // 0: softmax over the E logits, 1: sigmoid of each
+    int n_group;        // 1: no groups
+    int topk_group;
+    int group_top;      // a group's score: the sum of its 1 or 2 largest biased scores
+    int renorm;
+    float scale;
+    const float* bias;  // [E] or null
+};
+
+// The grouped products' work list: tile i of expert e covers rows mt*i .. of
+// its bucket (TileList, kernels.h), written by the routing launch when mt > 0.
+hipError_t launch_route_scored(const float* logits, int T, int E, int k, const ScoreRule& rule, const RoutingPtrs& r,
+                               void* ws, hipStream_t s);
+
+// ------------------------------------------------------------------ 8-bit float path
+
+constexpr int kFp8Block = 128;
+
+enum class ElemType { kF32, kF16, kBF16 };
+
+// One e4m3 matrix bank: n matrices of rows x cols codes, one fp32 scale per
+// 128 x 128 block.
+struct Fp8Mat {
+    const uint8_t* data;
+    const float* scale;
+    int64_t row_stride, expert_stride;   // bytes
+    int rows, cols;
+};
+
+hipError_t launch_quantize_fp8(const void* x, ElemType xt, int64_t ldx, int T, int H, uint8_t* xq, float* xs,
+                               hipStream_t s);
+
+struct Fp8MatmulArgs {
+    const uint8_t* xq;
+    const float* xs;
+    Fp8Mat w;
+    void* y;
+    ElemType yt;
+    int64_t ldy;
+    int T;
+};
+hipError_t launch_matmul_fp8(const Fp8MatmulArgs& a, hipStream_t s);
+
+struct Fp8FfnArgs {
+    Fp8Mat gate, up, down, sgate, sup, sdown;
+    int has_shared, H, I, T, k, E;
+    RoutingPtrs r;
+    const uint8_t* xq;       // [T][H]
+    const float* xs;         // [T][H/128]
+    uint8_t* hq;             // workspace [T*k (+T)][I], bucket order, then the shared expert's rows
+    float* hs;               // workspace [T*k (+T)][I/128]
+    void* y_pair;            // [T*k][H] fp32 or bf16
+    void* y_shared;          // [T][H], the same type
+    int pair_bf16;
+    int exact;               // products with fp32 sums throughout (fp8_gemm.hip)
+    int32_t* tiles;          // workspace: the work list (fp8_tiles_bytes)
+};
+size_t fp8_tiles_bytes(int T, int k, int E, int has_shared);
+hipError_t launch_ffn_fp8(const Fp8FfnArgs& a, hipStream_t s);
+
+struct Fp8CombineArgs {
+    const void* y_pair;      // fp32 or bf16 [T*k][H]
+    const void* y_shared;    // the same type [T][H], or null
+    int pair_bf16;
+    const float* w;          // [T][k]
+    const float* shared_scale;
+    void* out;
+    ElemType ot;
+    int T, k, H;
+};
+hipError_t launch_combine_fp8(const Fp8CombineArgs& a, hipStream_t s);
+
+// ------------------------------------------------------------------ device helpers
+
+__device__ __forceinline__ float elem_f32(float v) { return v; }
+__device__ __forceinline__ float elem_f32(_Float16 v) { return (float)v; }
+__device__ __forceinline__ float elem_f32(__bf16 v) { return (float)v; }
+
+// The quantiser's rule for one block: a = max|x| > 0 (finite), codes
+// e4m3(x * 448 / a), scale a / 448.  x * 448 / a is formed as t / m with
+// a = m * 2^e, 1 <= m < 2, t = x * (448 * 2^-e) (in range for every finite a
+// >= 2^-116; a smaller a counts as 2^-116) and one residual step on the
+// hardware reciprocal.  Where the quotient is an fp32 value (every tie between
+// two codes for bf16 and fp16 inputs is one) the step gives it exactly:
+// q0 is within 2 ulp, the residual t - q0*m is exact in an fma, and the
+// correction errs by 2^-23 of those 2 ulp.  So ties resolve to even as in
+// exact arithmetic.
+struct Fp8Rule {
+    float c, m, r, d;
+    __device__ __forceinline__ explicit Fp8Rule(float amax) {
+        const float a = fmaxf(amax, 0x1p-116f);
+        const uint32_t b = __float_as_uint(a);
+        c = __uint_as_float(((262u - (b >> 23)) << 23) | 0x600000u);   // 1.75 * 2^(8 - e)
+        m = __uint_as_float((b & 0x7FFFFFu) | 0x3F800000u);
+        r = __builtin_amdgcn_rcpf(m);
+        d = amax > 0.0f ? __fdiv_rn(a, 448.0f) : 0.0f;
+    }
+    __device__ __forceinline__ float quot(float x) const {
+        const float t = x * c;
+        const float q0 = t * r;
+        return fmaf(fmaf(-q0, m, t), r, q0);
+    }
+    // four values to four codes (round to nearest even; |quotient| <= 448*(1 + 2^-22), far below
+    // the 464 where rounding would leave the format)
+    __device__ __forceinline__ uint32_t pack4(float x0, float x1, float x2, float x3) const {
+        int v = __builtin_amdgcn_cvt_pk_fp8_f32(quot(x0), quot(x1), 0, false);
+        v = __builtin_amdgcn_cvt_pk_fp8_f32(quot(x2), quot(x3), v, true);
+        return (uint32_t)v;
+    }
+};
+
+}  // namespace moe

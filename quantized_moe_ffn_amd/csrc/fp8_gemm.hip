@@ -1,0 +1,600 @@
+// fp8_gemm.hip — products of e4m3 activations (one fp32 scale per row and 128
+// columns) with e4m3 weights (one per 128 x 128 block), dense and grouped by
+// expert, on v_mfma_f32_16x16x128_f8f6f4.
+//
+//   y[t][n] = sum_b xs[t][b] * ws[n/128][b] * sum_{j in block b} xq[t][j] * wq[n][j]
+//
+// One MFMA is exactly one scale block deep, so a block's partial sum is one
+// MFMA on a zero accumulator, and the running fp32 sum takes it with one fma
+// per value.
+//
+// Precision.  The 8-bit MFMA aligns each eight consecutive products to the
+// largest of them and keeps 13 bits below its exponent (measured: 8 of 65536 +
+// 14 survives, truncated towards zero), then adds the eights in fp32: about
+// 1.4e-5 of the result on normal data, at most 7 * 2^-13 of the eights'
+// largest products.  That is below a bf16 or fp16 store's rounding of a
+// product, and is used for those.  Results that keep more (fp32 products,
+// layers in fp32 or fp16, whose h decides between codes) take the EXACT
+// variant: the codes widened to fp16 (exact) and four
+// v_mfma_f32_16x16x32_f16, whose sums are fp32 throughout (measured 1e-8), at
+// half the matrix rate.  The weights are the MFMA's row operand and the tokens its column
+// operand: a lane then holds one token and four consecutive weight rows, so
+// its scale is a single product xs*ws per token tile and block.
+//
+// Tiles.  A workgroup takes NR weight rows x MT tokens; both operands pass
+// through LDS in 128-byte (one block deep) row slices, loaded straight from
+// global memory (global_load_lds_dwordx4: no registers, no ds_write), STAGES
+// deep.  A row's eight 16-byte chunks are stored at chunk ^ (row & 7), so the
+// eight rows a ds_read_b128 phase touches fall on different banks.
+//
+// Grouped modes: gate/up interleaves 16-row tiles of gate and up in one wave,
+// so SiLU(gate)*up is formed in registers, and its 128 rows of I are one scale
+// block of h, which is requantised in the epilogue; down scatters to the
+// per-pair rows.
+#include "fp8.h"
+
+namespace moe {
+
+namespace {
+
+typedef int v8i_f8 __attribute__((ext_vector_type(8)));
+typedef float v4f_f8 __attribute__((ext_vector_type(4)));
+
+__device__ __attribute__((aligned(16))) const uint32_t g_fp8_zero[4] = {0, 0, 0, 0};
+
+typedef _Float16 v8h_f8 __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h_f8 __attribute__((ext_vector_type(2)));
+
+// The block product of one 16-row and one 16-token fragment (32 codes of a
+// row or token per lane, the same columns in both).
+template <bool EXACT>
+struct Fp8Frag;
+
+template <>
+struct Fp8Frag<false> {
+    v8i_f8 v;
+    __device__ __forceinline__ void set(int4 a, int4 b) { v = v8i_f8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}; }
+    __device__ __forceinline__ v4f_f8 times(const Fp8Frag& o) const {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, o.v, v4f_f8{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+    }
+};
+
+template <>
+struct Fp8Frag<true> {
+    v8h_f8 v[4];
+    __device__ __forceinline__ static v8h_f8 widen(int lo, int hi) {
+        const v2h_f8 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+        const v2h_f8 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+        const v2h_f8 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+        const v2h_f8 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+        return v8h_f8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    }
+    __device__ __forceinline__ void set(int4 a, int4 b) {
+        v[0] = widen(a.x, a.y);
+        v[1] = widen(a.z, a.w);
+        v[2] = widen(b.x, b.y);
+        v[3] = widen(b.z, b.w);
+    }
+    __device__ __forceinline__ v4f_f8 times(const Fp8Frag& o) const {
+        v4f_f8 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[i], o.v[i], t, 0, 0, 0);
+        return t;
+    }
+};
+
+enum Fp8Mode { kFp8Dense, kFp8GateUp, kFp8Down };
+
+// One workgroup-wide asynchronous copy instruction of a wave: lane l's 16 (or
+// 4) bytes at src go to LDS byte lds + 16*l (or 4*l).  lds is wave-uniform.
+// The compiler does not count these loads (with its own builtin it waits for
+// all of them before any LDS read, which leaves no stage in flight); the
+// kernels wait on vmcnt themselves.  No output register is written, and the
+// kernels hold nothing in m0.
+__device__ __forceinline__ void copy16_lds(const void* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
+}
+__device__ __forceinline__ void copy4_lds(const void* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// All of this wave's LDS reads are in registers, then the workgroup meets.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+struct Fp8TileArgs {
+    Fp8Mat w0, w1;             // dense: w0; gate/up: gate, up; down: w0
+    Fp8Mat s0, s1;             // the shared expert's
+    const uint8_t* xq;         // token operand [rows][K]
+    const float* xs;           // [rows][K/128]
+    int K, N;                  // N: rows of one matrix
+    int T, k, E;
+    // dense
+    void* y;
+    ElemType yt;
+    int64_t ldy;
+    int vec_ok;                // 4-value stores are aligned
+    int n_mt;                  // token tiles
+    // grouped
+    const int32_t *count, *offset, *pair;
+    TileList tl;
+    uint8_t* hq;               // gate/up: out
+    float* hs;
+    void* y_pair;              // down: out
+    void* y_shared;
+    int pair_bf16;
+    int nblocks;               // row blocks
+};
+
+__device__ __forceinline__ void store4(void* base, int64_t idx, ElemType t, const float (&v)[4], int n_ok, bool vec) {
+    if (t == ElemType::kF32) {
+        float* p = (float*)base + idx;
+        if (vec && n_ok >= 4) {
+            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n_ok) p[i] = v[i];
+        }
+        return;
+    }
+    uint16_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[i] = t == ElemType::kF16 ? __builtin_bit_cast(uint16_t, (_Float16)v[i])
+                                   : __builtin_bit_cast(uint16_t, (__bf16)v[i]);
+    uint16_t* p = (uint16_t*)base + idx;
+    if (vec && n_ok >= 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n_ok) p[i] = h[i];
+    }
+}
+
+template <int NWN, int NWM, int WN, int WM, int STAGES>
+struct Fp8Tile {
+    static constexpr int kWaves = NWN * NWM;
+    static constexpr int kThreads = kWaves * kWave;
+    static constexpr int NR = NWN * WN * 16;
+    static constexpr int MT = NWM * WM * 16;
+    static constexpr int NA = NR / 8 / kWaves;   // weight copies of a wave per stage
+    static constexpr int NB = MT / 8 / kWaves;   // token copies
+    static constexpr int kLoads = NA + NB + 1;   // + the token scales
+    static constexpr int kScaleFloats = MT < 64 ? 64 : MT;
+    static constexpr int kStage = (NR + MT) * 128 + kScaleFloats * 4;
+    static constexpr int kLds = STAGES * kStage;
+    static_assert(NA * 8 * kWaves == NR && NB * 8 * kWaves == MT, "copies divide evenly");
+    static_assert(kLds <= 160 * 1024, "LDS");
+};
+
+template <int MODE, bool EXACT, int NWN, int NWM, int WN, int WM, int STAGES>
+__global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8TileArgs a) {
+    using C = Fp8Tile<NWN, NWM, WN, WM, STAGES>;
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+    __shared__ int s_row[C::MT];                 // output row of each token of the tile, -1: none
+    __shared__ uint32_t s_amax[MODE == kFp8GateUp ? NWN : 1][C::MT];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wn = wave % NWN, wm = wave / NWN;
+    const int K = a.K, KB = (K + kFp8Block - 1) / kFp8Block;
+
+    // the work item: weights, row block, tokens
+    Fp8Mat m0 = a.w0, m1 = a.w1;
+    int nb, mt0, n_tok, e = 0, off = 0;
+    bool shared = false;
+    if constexpr (MODE == kFp8Dense) {
+        // XCD x takes a contiguous range of items; inside it, bands of 8 row blocks
+        const int n_work = a.nblocks * a.n_mt;
+        const int chunk = (n_work + 7) / 8;
+        const int w = (blockIdx.x % 8) * chunk + blockIdx.x / 8;
+        if ((int)(blockIdx.x / 8) >= chunk || w >= n_work) return;
+        const int band = w / (8 * a.n_mt);
+        const int in = w - band * 8 * a.n_mt;
+        const int width = min(8, a.nblocks - band * 8);
+        nb = band * 8 + in % width;
+        mt0 = (in / width) * C::MT;
+        n_tok = min(C::MT, a.T - mt0);
+    } else {
+        const int n_work = *a.tl.n_tiles * a.nblocks;
+        const int chunk = (n_work + 7) / 8;
+        const int w = (blockIdx.x % 8) * chunk + blockIdx.x / 8;
+        if ((int)(blockIdx.x / 8) >= chunk || w >= n_work) return;
+        const int u = w / a.nblocks;
+        nb = w - u * a.nblocks;
+        e = a.tl.tile_e[u];
+        mt0 = a.tl.tile_m0[u];
+        shared = e >= a.E;
+        int c = a.T;
+        if (shared) {
+            m0 = a.s0;
+            m1 = a.s1;
+        } else {
+            c = a.count[e];
+            off = a.offset[e];
+            if (c < 0 || off < 0 || (int64_t)off + c > (int64_t)a.T * a.k) {   // buffers not from a routing pass
+                if (tid == 0) raise_error(kErrPairRange);
+                return;
+            }
+            m0.data += (int64_t)e * m0.expert_stride;
+            m0.scale += (int64_t)e * ((m0.rows + 127) / 128) * KB;
+            if constexpr (MODE == kFp8GateUp) {
+                m1.data += (int64_t)e * m1.expert_stride;
+                m1.scale += (int64_t)e * ((m1.rows + 127) / 128) * KB;
+            }
+        }
+        n_tok = min(C::MT, c - mt0);
+        for (int m = tid; m < C::MT; m += C::kThreads) {
+            int row = -1;
+            if (m < n_tok) {
+                row = shared ? mt0 + m : a.pair[off + mt0 + m];
+                if (!shared && (uint32_t)row >= (uint32_t)(a.T * a.k)) {
+                    raise_error(kErrPairRange);
+                    row = -1;
+                }
+            }
+            s_row[m] = row;
+        }
+        __syncthreads();
+        if (n_tok <= 0) return;
+    }
+    // source row of tile token m (a clamped valid row past the end)
+    auto src_row = [&](int m) -> int64_t {
+        m = min(m, n_tok - 1);
+        if constexpr (MODE == kFp8Dense) return mt0 + m;
+        if constexpr (MODE == kFp8Down) return (shared ? (int64_t)a.T * a.k : (int64_t)off) + mt0 + m;
+        const int row = s_row[m];
+        return shared ? row : max(row, 0) / a.k;
+    };
+
+    // copy sources: lane l of copy i holds row 8*(copy) + l/8, chunk (l%8) ^ (row%8)
+    const uint8_t* pa[C::NA];
+    const uint8_t* pb[C::NB];
+    const int lr = lane >> 3;
+    const int ca = ((lane & 7) ^ lr) * 16;   // the chunk's first column within a block (rows advance by multiples of 8)
+#pragma unroll
+    for (int i = 0; i < C::NA; ++i) {
+        const int R = (wave + i * C::kWaves) * 8 + lr;
+        if constexpr (MODE == kFp8GateUp) {
+            const int w_ = R / (WN * 16), t_ = (R / 16) % WN, r_ = R & 15;
+            const int row = nb * (C::NR / 2) + w_ * (WN / 2 * 16) + (t_ % (WN / 2)) * 16 + r_;
+            const Fp8Mat& m = t_ < WN / 2 ? m0 : m1;
+            pa[i] = m.data + (int64_t)row * m.row_stride + ca;
+        } else {
+            pa[i] = m0.data + (int64_t)min(nb * C::NR + R, a.N - 1) * m0.row_stride + ca;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < C::NB; ++i) {
+        const int R = (wave + i * C::kWaves) * 8 + lr;
+        pb[i] = a.xq + src_row(R) * K + ca;
+    }
+    const int seg = C::MT >= 64 ? wave % (C::MT / 64) : 0;
+    const float* ps = a.xs + src_row((C::MT >= 64 ? seg * 64 : 0) + lane) * KB;
+
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds;
+    auto issue = [&](int kb) {
+        const uint32_t st = lds0 + (kb % STAGES) * C::kStage;
+        const uint32_t la = st + wave * 1024, lb = la + C::NR * 128;
+        if ((kb + 1) * kFp8Block <= K) {
+#pragma unroll
+            for (int i = 0; i < C::NA; ++i) copy16_lds(pa[i] + kb * kFp8Block, la + i * C::kWaves * 1024);
+#pragma unroll
+            for (int i = 0; i < C::NB; ++i) copy16_lds(pb[i] + kb * kFp8Block, lb + i * C::kWaves * 1024);
+        } else {   // the last block of a K that is no multiple of 128: chunks past the last column read zeros
+            const bool live = kb * kFp8Block + ca < K;
+            const uintptr_t z = (uintptr_t)g_fp8_zero;
+#pragma unroll
+            for (int i = 0; i < C::NA; ++i)
+                copy16_lds((const void*)(live ? (uintptr_t)(pa[i] + kb * kFp8Block) : z), la + i * C::kWaves * 1024);
+#pragma unroll
+            for (int i = 0; i < C::NB; ++i)
+                copy16_lds((const void*)(live ? (uintptr_t)(pb[i] + kb * kFp8Block) : z), lb + i * C::kWaves * 1024);
+        }
+        copy4_lds(ps + kb, st + (C::NR + C::MT) * 128 + seg * 256);
+    };
+
+    // this wave's weight scales: lane l holds block l of a group of 64 blocks
+    const int n_first = MODE == kFp8GateUp ? nb * (C::NR / 2) : nb * C::NR + wn * WN * 16;
+    const int sb = min(n_first, a.N - 1) / kFp8Block;
+    const float* w0s = m0.scale + (int64_t)sb * KB;
+    const float* w1s = MODE == kFp8GateUp ? m1.scale + (int64_t)sb * KB : nullptr;
+    float ws0 = w0s[min(lane, KB - 1)], ws1 = MODE == kFp8GateUp ? w1s[min(lane, KB - 1)] : 0.f;
+
+    v4f_f8 acc[WN][WM] = {};
+    const int g = lane >> 4, r16 = lane & 15;
+    const int c0 = ((2 * g) ^ (r16 & 7)) * 16, c1 = ((2 * g + 1) ^ (r16 & 7)) * 16;
+
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        if (s < KB) issue(s);
+    for (int kb = 0; kb < KB; ++kb) {
+        if ((kb & 63) == 0 && kb > 0) {   // the compiler waits on these (and so on every older copy) at their use
+            ws0 = w0s[min(kb + lane, KB - 1)];
+            if constexpr (MODE == kFp8GateUp) ws1 = w1s[min(kb + lane, KB - 1)];
+        }
+        if (kb + STAGES - 2 < KB)
+            wait_vm<(STAGES - 2) * C::kLoads>();
+        else
+            wait_vm<0>();
+        lds_barrier();
+        if (kb + STAGES - 1 < KB) issue(kb + STAGES - 1);
+        const unsigned char* st = lds + (kb % STAGES) * C::kStage;
+        const float wb0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ws0), kb & 63));
+        const float wb1 = MODE == kFp8GateUp
+                              ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ws1), kb & 63))
+                              : 0.f;
+        Fp8Frag<EXACT> fa[WN];
+#pragma unroll
+        for (int i = 0; i < WN; ++i) {
+            const unsigned char* p = st + ((wn * WN + i) * 16 + r16) * 128;
+            fa[i].set(*reinterpret_cast<const int4*>(p + c0), *reinterpret_cast<const int4*>(p + c1));
+        }
+        const float* sx = reinterpret_cast<const float*>(st + (C::NR + C::MT) * 128);
+#pragma unroll
+        for (int j = 0; j < WM; ++j) {
+            const int m = (wm * WM + j) * 16 + r16;
+            const unsigned char* p = st + C::NR * 128 + m * 128;
+            Fp8Frag<EXACT> fb;
+            fb.set(*reinterpret_cast<const int4*>(p + c0), *reinterpret_cast<const int4*>(p + c1));
+            const float x = sx[m];
+            const float s0 = x * wb0, s1 = MODE == kFp8GateUp ? x * wb1 : 0.f;
+#pragma unroll
+            for (int i = 0; i < WN; ++i) {
+                const v4f_f8 t = fa[i].times(fb);
+                const float s = MODE == kFp8GateUp && i >= WN / 2 ? s1 : s0;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(t[v], s, acc[i][j][v]);
+            }
+        }
+    }
+
+    // value v of acc[i][j]: weight row 16*i + 4*g + v of the wave, token 16*j + r16 of the wave
+    if constexpr (MODE == kFp8Dense) {
+#pragma unroll
+        for (int j = 0; j < WM; ++j) {
+            const int m = (wm * WM + j) * 16 + r16;
+            if (m >= n_tok) continue;
+#pragma unroll
+            for (int i = 0; i < WN; ++i) {
+                const int n = nb * C::NR + (wn * WN + i) * 16 + 4 * g;
+                const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                if (n < a.N) store4(a.y, (int64_t)(mt0 + m) * a.ldy + n, a.yt, v, a.N - n, a.vec_ok);
+            }
+        }
+    } else if constexpr (MODE == kFp8Down) {
+        const ElemType pt = a.pair_bf16 ? ElemType::kBF16 : ElemType::kF32;
+        void* base = shared ? a.y_shared : a.y_pair;
+#pragma unroll
+        for (int j = 0; j < WM; ++j) {
+            const int row = s_row[(wm * WM + j) * 16 + r16];
+            if (row < 0) continue;
+#pragma unroll
+            for (int i = 0; i < WN; ++i) {
+                const int n = nb * C::NR + (wn * WN + i) * 16 + 4 * g;
+                const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                if (n < a.N) store4(base, (int64_t)row * a.N + n, pt, v, a.N - n, true);
+            }
+        }
+    } else {
+        constexpr int HI = WN / 2;
+        // h = silu(gate) * up in place of the gate sums; the block's maximum over the wave's rows, then over the waves
+#pragma unroll
+        for (int j = 0; j < WM; ++j) {
+            uint32_t mx = 0;
+#pragma unroll
+            for (int i = 0; i < HI; ++i)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float h = silu_f32(acc[i][j][v]) * acc[i + HI][j][v];
+                    acc[i][j][v] = h;
+                    mx = max(mx, __float_as_uint(h) & 0x7FFFFFFFu);
+                }
+            mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, kWave));
+            mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, kWave));
+            if (g == 0) s_amax[wn][(wm * WM + j) * 16 + r16] = mx;
+        }
+        __syncthreads();
+        const int64_t row0 = (shared ? (int64_t)a.T * a.k : (int64_t)off) + mt0;
+#pragma unroll
+        for (int j = 0; j < WM; ++j) {
+            const int m = (wm * WM + j) * 16 + r16;
+            if (m >= n_tok) continue;
+            uint32_t mx = s_amax[0][m];
+#pragma unroll
+            for (int q = 1; q < NWN; ++q) mx = max(mx, s_amax[q][m]);
+            const bool fin = mx < 0x7F800000u;
+            if (!fin) raise_error(kErrActNonFinite);
+            const Fp8Rule rule(__uint_as_float(fin ? mx : 0u));
+#pragma unroll
+            for (int i = 0; i < HI; ++i) {
+                const uint32_t q = fin ? rule.pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]) : 0u;
+                const int col = nb * (C::NR / 2) + (wn * HI + i) * 16 + 4 * g;
+                *reinterpret_cast<uint32_t*>(a.hq + (row0 + m) * a.N + col) = q;
+            }
+            if (wn == 0 && g == 0) a.hs[(row0 + m) * (a.N / kFp8Block) + nb] = rule.d;
+        }
+    }
+}
+
+// The work list of the grouped products from the bucket counts.
+__global__ void __launch_bounds__(1024) fp8_tiles_kernel(const int32_t* count, int npairs, int E, TileList tl) {
+    __shared__ int s_wave[kWave + 1];
+    __shared__ int s_start[1024];
+    const int tid = threadIdx.x;
+    write_tile_list(tid < E ? count[tid] : 0, npairs, E, tl, s_wave, s_start);
+}
+
+template <int MODE, bool EXACT, int NWN, int NWM, int WN, int WM, int STAGES>
+hipError_t launch_tile(const Fp8TileArgs& a, int64_t n_work, hipStream_t s) {
+    using C = Fp8Tile<NWN, NWM, WN, WM, STAGES>;
+    const unsigned grid = (unsigned)((n_work + 7) / 8 * 8);
+    fp8_tile_kernel<MODE, EXACT, NWN, NWM, WN, WM, STAGES><<<grid, C::kThreads, C::kLds, s>>>(a);
+    return hipGetLastError();
+}
+
+int fp8_tile_tokens(int T, int k, int E) {
+    const int64_t per = ((int64_t)T * k + E - 1) / E;
+    return per <= 32 ? 32 : (per <= 64 ? 64 : 128);
+}
+
+int fp8_max_tiles(int T, int k, int E, int has_shared, int mt) {
+    const int64_t P = (int64_t)T * k;
+    const int64_t act = P < E ? P : E;
+    return (int)(P / mt + act + (has_shared ? (T + mt - 1) / mt : 0));
+}
+
+template <int MODE, bool EXACT>
+hipError_t launch_grouped(const Fp8TileArgs& a, int64_t n_work, hipStream_t s) {
+    if (a.tl.mt == 32) return launch_tile<MODE, EXACT, 4, 1, 4, 2, 2>(a, n_work, s);
+    if (a.tl.mt == 64) return launch_tile<MODE, EXACT, 4, 2, 4, 2, 3>(a, n_work, s);
+    return launch_tile<MODE, EXACT, 4, 2, 4, 4, 3>(a, n_work, s);
+}
+
+template <bool EXACT>
+hipError_t launch_dense(const Fp8TileArgs& a, int mt, int64_t n_work, hipStream_t s) {
+    if (mt == 32) return launch_tile<kFp8Dense, EXACT, 4, 1, 4, 2, 2>(a, n_work, s);
+    if (mt == 64) return launch_tile<kFp8Dense, EXACT, 4, 2, 4, 2, 3>(a, n_work, s);
+    if (mt == 128) return launch_tile<kFp8Dense, EXACT, 4, 2, 4, 4, 3>(a, n_work, s);
+    return launch_tile<kFp8Dense, false, 4, 2, 4, 8, 2>(a, n_work, s);
+}
+
+}  // namespace
+
+size_t fp8_tiles_bytes(int T, int k, int E, int has_shared) {
+    return (size_t)(2 * (int64_t)fp8_max_tiles(T, k, E, has_shared, fp8_tile_tokens(T, k, E)) + 1) * sizeof(int32_t);
+}
+
+hipError_t launch_ffn_fp8(const Fp8FfnArgs& f, hipStream_t s) {
+    const int mt = fp8_tile_tokens(f.T, f.k, f.E);
+    const int max_t = fp8_max_tiles(f.T, f.k, f.E, f.has_shared, mt);
+    TileList tl{};
+    tl.tile_e = f.tiles;
+    tl.tile_m0 = f.tiles + max_t;
+    tl.n_tiles = f.tiles + 2 * (int64_t)max_t;
+    tl.mt = mt;
+    tl.max_t = max_t;
+    tl.T = f.T;
+    tl.has_shared = f.has_shared;
+    fp8_tiles_kernel<<<1, 1024, 0, s>>>(f.r.count, f.T * f.k, f.E, tl);
+    Fp8TileArgs a{};
+    a.w0 = f.gate;
+    a.w1 = f.up;
+    a.s0 = f.sgate;
+    a.s1 = f.sup;
+    a.xq = f.xq;
+    a.xs = f.xs;
+    a.K = f.H;
+    a.N = f.I;
+    a.T = f.T;
+    a.k = f.k;
+    a.E = f.E;
+    a.count = f.r.count;
+    a.offset = f.r.offset;
+    a.pair = f.r.pair;
+    a.tl = tl;
+    a.hq = f.hq;
+    a.hs = f.hs;
+    a.nblocks = f.I / kFp8Block;
+    hipError_t e = f.exact ? launch_grouped<kFp8GateUp, true>(a, (int64_t)max_t * a.nblocks, s)
+                           : launch_grouped<kFp8GateUp, false>(a, (int64_t)max_t * a.nblocks, s);
+    if (e != hipSuccess) return e;
+    a.w0 = f.down;
+    a.s0 = f.sdown;
+    a.xq = f.hq;
+    a.xs = f.hs;
+    a.K = f.I;
+    a.N = f.H;
+    a.y_pair = f.y_pair;
+    a.y_shared = f.y_shared;
+    a.pair_bf16 = f.pair_bf16;
+    a.nblocks = (f.H + 255) / 256;
+    return f.exact ? launch_grouped<kFp8Down, true>(a, (int64_t)max_t * a.nblocks, s)
+                   : launch_grouped<kFp8Down, false>(a, (int64_t)max_t * a.nblocks, s);
+}
+
+hipError_t launch_matmul_fp8(const Fp8MatmulArgs& m, hipStream_t s) {
+    Fp8TileArgs a{};
+    a.w0 = m.w;
+    a.xq = m.xq;
+    a.xs = m.xs;
+    a.K = m.w.cols;
+    a.N = m.w.rows;
+    a.T = m.T;
+    a.y = m.y;
+    a.yt = m.yt;
+    a.ldy = m.ldy;
+    const int sz = m.yt == ElemType::kF32 ? 4 : 2;
+    a.vec_ok = m.ldy % 4 == 0 && (uintptr_t)m.y % (4 * sz) == 0;
+    a.nblocks = (m.w.rows + 255) / 256;
+    const bool exact = m.yt == ElemType::kF32;
+    const int mt = m.T <= 32 ? 32 : (m.T <= 64 ? 64 : (m.T <= 512 || exact ? 128 : 256));
+    a.n_mt = (m.T + mt - 1) / mt;
+    const int64_t n_work = (int64_t)a.nblocks * a.n_mt;
+    return exact ? launch_dense<true>(a, mt, n_work, s) : launch_dense<false>(a, mt, n_work, s);
+}
+
+// ---------------------------------------------------------------------------
+// Combine: out[t] = sum_j w[t][j] * y_pair[t*k+j] (slot order), then the shared
+// expert's, summed in fp32 and rounded once.  Eight values per thread; HBM-bound.
+// ---------------------------------------------------------------------------
+namespace {
+
+__device__ __forceinline__ void load8_pair(const void* base, int bf16, int64_t idx, float (&v)[8]) {
+    if (bf16) {
+        const uint4 q = *reinterpret_cast<const uint4*>((const uint16_t*)base + idx);
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+    } else {
+        const float4* p = reinterpret_cast<const float4*>((const float*)base + idx);
+        const float4 a = p[0], b = p[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+}
+
+__global__ void __launch_bounds__(256) combine_fp8_kernel(const Fp8CombineArgs a) {
+    const int H8 = a.H / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)a.T * H8) return;
+    const int64_t t = i / H8;
+    const int o = (int)(i - t * H8) * 8;
+    float acc[8] = {};
+    for (int j = 0; j < a.k; ++j) {
+        float v[8];
+        load8_pair(a.y_pair, a.pair_bf16, (t * a.k + j) * a.H + o, v);
+        const float w = a.w[t * a.k + j];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[q] = fmaf(w, v[q], acc[q]);
+    }
+    if (a.y_shared) {
+        float v[8];
+        load8_pair(a.y_shared, a.pair_bf16, t * a.H + o, v);
+        const float w = a.shared_scale ? a.shared_scale[t] : 1.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[q] = fmaf(w, v[q], acc[q]);
+    }
+    const float lo[4] = {acc[0], acc[1], acc[2], acc[3]}, hi[4] = {acc[4], acc[5], acc[6], acc[7]};
+    store4(a.out, t * a.H + o, a.ot, lo, 4, true);
+    store4(a.out, t * a.H + o + 4, a.ot, hi, 4, true);
+}
+
+}  // namespace
+
+hipError_t launch_combine_fp8(const Fp8CombineArgs& a, hipStream_t s) {
+    const int64_t n = (int64_t)a.T * (a.H / 8);
+    combine_fp8_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace moe
