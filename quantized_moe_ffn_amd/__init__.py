@@ -388,6 +388,15 @@ def moe_check_device_errors(stream=None):
 # ----------------------------------------------------------------------------- scored routing, 8-bit floats
 
 _elem_ids = None
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _elem_id(t) -> int:
@@ -402,31 +411,29 @@ def _elem_id(t) -> int:
     return i
 
 
-def _need(name: str, t, itemsize: int, shape, device=None, integer: bool | None = None):
-    """Checks a tensor argument: element size, shape, contiguity and device."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.element_size() != itemsize or t.is_complex() or (integer is not None and t.is_floating_point() == integer):
-        raise ValueError("%s has dtype %s" % (name, t.dtype))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+def _need(name: str, t, dtype, shape, device):
+    """Checks a tensor argument: type, shape, contiguity and device (kept light: it runs at every call)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s: %s %s on %s%s, expected %s %s on %s, contiguous"
+                         % (name, t.dtype, tuple(t.shape), t.device, "" if t.is_contiguous() else " (not contiguous)",
+                            dtype, tuple(shape), device))
 
 
 def _fp8_codes(name: str, t):
-    import torch
-    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    if t.dtype is not _torch().float8_e4m3fn and t.dtype is not _torch().uint8:
         raise ValueError("%s has dtype %s: e4m3 codes are float8_e4m3fn or uint8" % (name, t.dtype))
 
 
 def _launch_stream(device, stream) -> int:
     """The stream of a call on tensors of `device`, which has to be the current one."""
-    import torch
     if device.type != "cuda":
         raise ValueError("tensors must be on a GPU, got %s" % device)
-    if device.index != torch.cuda.current_device():
-        raise ValueError("tensors are on %s, the current device is cuda:%d" % (device, torch.cuda.current_device()))
+    torch = _torch()
+    cur = torch._C._cuda_getDevice()
+    if device.index != cur:
+        raise ValueError("tensors are on %s, the current device is cuda:%d" % (device, cur))
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(cur)
     return _stream(stream)
 
 
@@ -440,7 +447,7 @@ class RouteSpec:
         if score not in ("softmax", "sigmoid"):
             raise ValueError("score = %r: use 'softmax' or 'sigmoid'" % (score,))
         if bias is not None:
-            _need("bias", bias, 4, (bias.numel(),), integer=False)
+            _need("bias", bias, _torch().float32, (bias.numel(),), bias.device)
         self.bias = bias
         self._s = moe_route_spec(MOE_SCORE_SIGMOID if score == "sigmoid" else MOE_SCORE_SOFTMAX, n_group, topk_group,
                                  group_top, 1 if renorm else 0, scale, _ptr(bias))
@@ -466,7 +473,7 @@ class Fp8Matrix:
         if cols > 1 and data.stride(2) != 1:
             raise ValueError("data: columns must be contiguous")
         b = MOE_FP8_BLOCK
-        _need("scale", scale, 4, (n, (rows + b - 1) // b, (cols + b - 1) // b), data.device, integer=False)
+        _need("scale", scale, _torch().float32, (n, (rows + b - 1) // b, (cols + b - 1) // b), data.device)
         self.data, self.scale, self.n, self.rows, self.cols = data, scale, n, rows, cols
         self._s = moe_fp8_matrix(data.data_ptr(), scale.data_ptr(), rows, cols,
                                  data.stride(1) if rows > 1 else (cols + 15) // 16 * 16,
@@ -504,7 +511,7 @@ class Fp8Layer:
 
 
 def _check_routing(routing: Routing, T: int, E: int, k: int, device):
-    if (routing.T, routing.E, routing.k) != (T, E, k) or routing.idx.device != device:
+    if routing.T != T or routing.E != E or routing.k != k or routing.idx.device != device:
         raise ValueError("routing buffers are for T, E, k = %d, %d, %d on %s, expected %d, %d, %d on %s"
                          % (routing.T, routing.E, routing.k, routing.idx.device, T, E, k, device))
 
@@ -520,7 +527,7 @@ def _ws(workspace, device):
 def moe_route_scored(logits, k: int, routing: Routing, spec: RouteSpec, workspace=None, stream=None):
     """Expert selection by a score rule, with moe_route_topk's buffers and workspace (fp32 logits [T][E])."""
     T, E = logits.shape
-    _need("logits", logits, 4, (T, E), integer=False)
+    _need("logits", logits, _torch().float32, (T, E), logits.device)
     _check_routing(routing, T, E, k, logits.device)
     spec.check(E, logits.device)
     wp, wn = _ws(workspace, logits.device)
@@ -535,11 +542,12 @@ def moe_quantize_fp8(x, xq, xs, stream=None):
     T, H = x.shape
     if x.stride(1) != 1 and H > 1:
         raise ValueError("x: columns must be contiguous")
+    d = x.device
     _fp8_codes("xq", xq)
-    _need("xq", xq, 1, (T, H), x.device)
-    _need("xs", xs, 4, (T, (H + MOE_FP8_BLOCK - 1) // MOE_FP8_BLOCK), x.device, integer=False)
+    _need("xq", xq, xq.dtype, (T, H), d)
+    _need("xs", xs, _torch().float32, (T, (H + MOE_FP8_BLOCK - 1) // MOE_FP8_BLOCK), d)
     _check(load_library().moe_quantize_fp8(x.data_ptr(), _elem_id(x), x.stride(0) if T > 1 else H, T, H,
-                                           xq.data_ptr(), xs.data_ptr(), _launch_stream(x.device, stream)),
+                                           xq.data_ptr(), xs.data_ptr(), _launch_stream(d, stream)),
            "moe_quantize_fp8")
 
 
@@ -548,16 +556,17 @@ def moe_matmul_fp8(xq, xs, w: Fp8Matrix, y, stream=None):
     y float32, float16 or bfloat16, columns contiguous, rows at any distance."""
     T, K = xq.shape
     _fp8_codes("xq", xq)
-    _need("xq", xq, 1, (T, w.cols), w.data.device)
-    _need("xs", xs, 4, (T, w.scale.shape[2]), w.data.device, integer=False)
+    d = w.data.device
+    _need("xq", xq, xq.dtype, (T, w.cols), d)
+    _need("xs", xs, _torch().float32, (T, w.scale.shape[2]), d)
     if w.n != 1:
         raise ValueError("w holds %d matrices, expected one" % w.n)
-    if tuple(y.shape) != (T, w.rows) or (y.stride(1) != 1 and w.rows > 1) or y.device != w.data.device:
+    if y.shape != (T, w.rows) or (y.stride(1) != 1 and w.rows > 1) or y.device != d:
         raise ValueError("y has shape %s, strides %s on %s: expected %s, contiguous columns, on %s"
-                         % (tuple(y.shape), y.stride(), y.device, (T, w.rows), w.data.device))
+                         % (tuple(y.shape), y.stride(), y.device, (T, w.rows), d))
     _check(load_library().moe_matmul_fp8(xq.data_ptr(), xs.data_ptr(), T, ctypes.byref(w.struct()), y.data_ptr(),
                                          _elem_id(y), y.stride(0) if T > 1 else w.rows,
-                                         _launch_stream(y.device, stream)), "moe_matmul_fp8")
+                                         _launch_stream(d, stream)), "moe_matmul_fp8")
 
 
 def moe_ffn_fp8_workspace_bytes(layer: Fp8Layer, T: int, k: int) -> int:
@@ -569,11 +578,12 @@ def moe_expert_ffn_fp8(layer: Fp8Layer, routing: Routing, T: int, k: int, y_pair
     H, d = layer.hidden, layer.device
     _check_routing(routing, T, layer.n_experts, k, d)
     _fp8_codes("xq", xq)
-    _need("xq", xq, 1, (T, H), d)
-    _need("xs", xs, 4, (T, H // MOE_FP8_BLOCK), d, integer=False)
-    _need("y_pair", y_pair, 4, (T * k, H), d, integer=False)
+    f32 = _torch().float32
+    _need("xq", xq, xq.dtype, (T, H), d)
+    _need("xs", xs, f32, (T, H // MOE_FP8_BLOCK), d)
+    _need("y_pair", y_pair, f32, (T * k, H), d)
     if y_shared is not None:
-        _need("y_shared", y_shared, 4, (T, H), d, integer=False)
+        _need("y_shared", y_shared, f32, (T, H), d)
     wp, wn = _ws(workspace, d)
     st = load_library().moe_expert_ffn_fp8(ctypes.byref(layer.struct()), ctypes.byref(routing.struct()), T, k,
                                            xq.data_ptr(), xs.data_ptr(), y_pair.data_ptr(), _ptr(y_shared), wp, wn,
@@ -590,14 +600,13 @@ def moe_forward_fp8(layer: Fp8Layer, logits, x, k: int, routing: Routing, spec: 
     """The whole layer over e4m3 experts from fp32 logits [T][E] and x [T][H] (out has x's type; it may be x)."""
     T, E = logits.shape
     d = layer.device
-    _need("logits", logits, 4, (T, layer.n_experts), d, integer=False)
+    f32 = _torch().float32
+    _need("logits", logits, f32, (T, layer.n_experts), d)
     xt = _elem_id(x)
-    _need("x", x, x.element_size(), (T, layer.hidden), d)
-    _need("out", out, x.element_size(), (T, layer.hidden), d)
-    if out.dtype != x.dtype:
-        raise ValueError("out has dtype %s, expected x's %s" % (out.dtype, x.dtype))
+    _need("x", x, x.dtype, (T, layer.hidden), d)
+    _need("out", out, x.dtype, (T, layer.hidden), d)
     if shared_scale is not None:
-        _need("shared_scale", shared_scale, 4, (T,), d, integer=False)
+        _need("shared_scale", shared_scale, f32, (T,), d)
     _check_routing(routing, T, E, k, d)
     spec.check(E, d)
     wp, wn = _ws(workspace, d)

@@ -70,9 +70,15 @@ struct Fp8FfnArgs {
     int pair_bf16;
     int exact;               // products with fp32 sums throughout (fp8_gemm.hip)
     int32_t* tiles;          // workspace: the work list (fp8_tiles_bytes)
+    float* hf;               // workspace of the few-pair kernels: h in fp32, [T*k (+T)][I]
 };
 size_t fp8_tiles_bytes(int T, int k, int E, int has_shared);
 hipError_t launch_ffn_fp8(const Fp8FfnArgs& a, hipStream_t s);
+
+// Few pairs: T*k up to this, and up to the expert count, so that few pairs share an expert's read.
+constexpr int kFewPairs = 64;
+constexpr int kMaxSlots = 17;   // top-k and the shared expert
+inline bool fp8_few_pairs(int T, int k, int E) { return T * k <= kFewPairs && T * k <= E; }
 
 struct Fp8CombineArgs {
     const void* y_pair;      // fp32 or bf16 [T*k][H]
@@ -84,6 +90,9 @@ struct Fp8CombineArgs {
     ElemType ot;
     int T, k, H;
 };
+// c.out null: y_pair and y_shared (fp32) instead of the combined output
+hipError_t launch_skinny_ffn(const Fp8FfnArgs& f, const Fp8CombineArgs& c, hipStream_t s);
+hipError_t launch_skinny_matmul(const Fp8MatmulArgs& a, hipStream_t s);
 hipError_t launch_combine_fp8(const Fp8CombineArgs& a, hipStream_t s);
 
 // ------------------------------------------------------------------ device helpers
@@ -122,6 +131,49 @@ struct Fp8Rule {
         int v = __builtin_amdgcn_cvt_pk_fp8_f32(quot(x0), quot(x1), 0, false);
         v = __builtin_amdgcn_cvt_pk_fp8_f32(quot(x2), quot(x3), v, true);
         return (uint32_t)v;
+    }
+};
+
+typedef int v8i_f8 __attribute__((ext_vector_type(8)));
+typedef float v4f_f8 __attribute__((ext_vector_type(4)));
+typedef _Float16 v8h_f8 __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h_f8 __attribute__((ext_vector_type(2)));
+
+// The block product of one 16-row and one 16-token fragment (32 codes of a
+// row or token per lane, the same columns in both).
+template <bool EXACT>
+struct Fp8Frag;
+
+template <>
+struct Fp8Frag<false> {
+    v8i_f8 v;
+    __device__ __forceinline__ void set(int4 a, int4 b) { v = v8i_f8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}; }
+    __device__ __forceinline__ v4f_f8 times(const Fp8Frag& o) const {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, o.v, v4f_f8{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+    }
+};
+
+template <>
+struct Fp8Frag<true> {
+    v8h_f8 v[4];
+    __device__ __forceinline__ static v8h_f8 widen(int lo, int hi) {
+        const v2h_f8 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+        const v2h_f8 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+        const v2h_f8 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+        const v2h_f8 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+        return v8h_f8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    }
+    __device__ __forceinline__ void set(int4 a, int4 b) {
+        v[0] = widen(a.x, a.y);
+        v[1] = widen(a.z, a.w);
+        v[2] = widen(b.x, b.y);
+        v[3] = widen(b.z, b.w);
+    }
+    __device__ __forceinline__ v4f_f8 times(const Fp8Frag& o) const {
+        v4f_f8 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[i], o.v[i], t, 0, 0, 0);
+        return t;
     }
 };
 

@@ -103,13 +103,17 @@ moe_status check_fp8_layer(const moe_fp8_layer* L, int T, int k) {
 }
 
 struct Fp8FfnWorkspace {
-    size_t hq, hs, tiles, total;
+    size_t hq, hs, tiles, hf, total;
 };
 
 Fp8FfnWorkspace fp8_ffn_layout(const moe_fp8_layer* L, int T, int k) {
     const size_t rows = (size_t)T * k + (L->has_shared ? T : 0);
     Fp8FfnWorkspace w{};
     size_t off = 0;
+    if (moe::fp8_few_pairs(T, k, L->n_experts)) {
+        w.total = align_up(rows * L->inter * sizeof(float), 256);
+        return w;
+    }
     w.hq = off;
     off += align_up(rows * L->inter, 256);
     w.hs = off;
@@ -136,6 +140,10 @@ Fp8ForwardWorkspace fp8_forward_layout(const moe_fp8_layer* L, int T, int k, boo
     off += align_up((size_t)T * L->hidden, 256);
     w.xs = off;
     off += align_up((size_t)T * (L->hidden / MOE_FP8_BLOCK) * sizeof(float), 256);
+    if (moe::fp8_few_pairs(T, k, L->n_experts)) {   // combined inside the down kernel
+        w.total = off;
+        return w;
+    }
     w.yp = off;
     off += align_up((size_t)T * k * L->hidden * (bf16 ? 2 : 4), 256);
     w.ysh = off;
@@ -165,6 +173,7 @@ moe::Fp8FfnArgs fp8_ffn_args(const moe_fp8_layer* L, const moe_routing* r, int T
     a.hq = (uint8_t*)(ws + w.hq);
     a.hs = (float*)(ws + w.hs);
     a.tiles = (int32_t*)(ws + w.tiles);
+    a.hf = (float*)(ws + w.hf);
     return a;
 }
 
@@ -231,8 +240,8 @@ moe_status moe_expert_ffn_fp8(const moe_fp8_layer* L, const moe_routing* r, int3
                               hipStream_t stream) {
     moe_status st = check_fp8_layer(L, T, k);
     if (st != MOE_OK) return st;
-    if (!r || !r->count || !r->offset || !r->pair || !r->active || !r->n_active)
-        return fail(MOE_ERR_INVALID_ARGUMENT, "moe_routing or one of count/offset/pair/active/n_active is NULL");
+    if (!r || !r->idx || !r->count || !r->offset || !r->pair || !r->active || !r->n_active)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "moe_routing or one of idx/count/offset/pair/active/n_active is NULL");
     if (!xq || !xs || !y_pair) return fail(MOE_ERR_INVALID_ARGUMENT, "xq, xs or y_pair is NULL");
     if (L->has_shared && !y_shared)
         return fail(MOE_ERR_INVALID_ARGUMENT, "layer has a shared expert but y_shared is NULL");
@@ -248,6 +257,9 @@ moe_status moe_expert_ffn_fp8(const moe_fp8_layer* L, const moe_routing* r, int3
     a.y_pair = y_pair;
     a.y_shared = y_shared;
     a.exact = 1;
+    if (moe::fp8_few_pairs(T, k, L->n_experts))
+        return finish(from_hip(moe::launch_skinny_ffn(a, moe::Fp8CombineArgs{}, stream), "moe_expert_ffn_fp8 launch"),
+                      stream, "moe_expert_ffn_fp8");
     return finish(from_hip(moe::launch_ffn_fp8(a, stream), "moe_expert_ffn_fp8 launch"), stream, "moe_expert_ffn_fp8");
 }
 
@@ -291,9 +303,12 @@ moe_status moe_forward_fp8(const moe_fp8_layer* L, const moe_route_spec* spec, c
     if (e != hipSuccess) return from_hip(e, "moe_forward_fp8: routing launch");
     e = moe::launch_quantize_fp8(x, xt, L->hidden, T, L->hidden, (uint8_t*)(ws + wl.xq), (float*)(ws + wl.xs), stream);
     if (e != hipSuccess) return from_hip(e, "moe_forward_fp8: quantisation launch");
+    const moe::Fp8CombineArgs c{a.y_pair, a.y_shared, a.pair_bf16, r->w, shared_scale, out, xt, T, k, L->hidden};
+    if (moe::fp8_few_pairs(T, k, L->n_experts))
+        return finish(from_hip(moe::launch_skinny_ffn(a, c, stream), "moe_forward_fp8: expert FFN launch"), stream,
+                      "moe_forward_fp8");
     e = moe::launch_ffn_fp8(a, stream);
     if (e != hipSuccess) return from_hip(e, "moe_forward_fp8: expert FFN launch");
-    const moe::Fp8CombineArgs c{a.y_pair, a.y_shared, a.pair_bf16, r->w, shared_scale, out, xt, T, k, L->hidden};
     return finish(from_hip(moe::launch_combine_fp8(c, stream), "moe_forward_fp8: combine launch"), stream,
                   "moe_forward_fp8");
 }

@@ -37,51 +37,7 @@ namespace moe {
 
 namespace {
 
-typedef int v8i_f8 __attribute__((ext_vector_type(8)));
-typedef float v4f_f8 __attribute__((ext_vector_type(4)));
-
 __device__ __attribute__((aligned(16))) const uint32_t g_fp8_zero[4] = {0, 0, 0, 0};
-
-typedef _Float16 v8h_f8 __attribute__((ext_vector_type(8)));
-typedef _Float16 v2h_f8 __attribute__((ext_vector_type(2)));
-
-// The block product of one 16-row and one 16-token fragment (32 codes of a
-// row or token per lane, the same columns in both).
-template <bool EXACT>
-struct Fp8Frag;
-
-template <>
-struct Fp8Frag<false> {
-    v8i_f8 v;
-    __device__ __forceinline__ void set(int4 a, int4 b) { v = v8i_f8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}; }
-    __device__ __forceinline__ v4f_f8 times(const Fp8Frag& o) const {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, o.v, v4f_f8{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-    }
-};
-
-template <>
-struct Fp8Frag<true> {
-    v8h_f8 v[4];
-    __device__ __forceinline__ static v8h_f8 widen(int lo, int hi) {
-        const v2h_f8 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
-        const v2h_f8 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
-        const v2h_f8 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
-        const v2h_f8 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
-        return v8h_f8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-    }
-    __device__ __forceinline__ void set(int4 a, int4 b) {
-        v[0] = widen(a.x, a.y);
-        v[1] = widen(a.z, a.w);
-        v[2] = widen(b.x, b.y);
-        v[3] = widen(b.z, b.w);
-    }
-    __device__ __forceinline__ v4f_f8 times(const Fp8Frag& o) const {
-        v4f_f8 t = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[i], o.v[i], t, 0, 0, 0);
-        return t;
-    }
-};
 
 enum Fp8Mode { kFp8Dense, kFp8GateUp, kFp8Down };
 
@@ -521,6 +477,7 @@ hipError_t launch_ffn_fp8(const Fp8FfnArgs& f, hipStream_t s) {
 }
 
 hipError_t launch_matmul_fp8(const Fp8MatmulArgs& m, hipStream_t s) {
+    if (m.T <= 32 || (int64_t)((m.w.rows + 255) / 256) * ((m.T + 127) / 128) < 64) return launch_skinny_matmul(m, s);
     Fp8TileArgs a{};
     a.w0 = m.w;
     a.xq = m.xq;

@@ -5,5 +5,6 @@
 
 #include "route_scored.hip"
 #include "fp8_quant.hip"
+#include "fp8_skinny.hip"
 #include "fp8_gemm.hip"
 #include "fp8_api.hip"

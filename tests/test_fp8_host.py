@@ -144,7 +144,9 @@ def test_workspaces_grow_with_the_work():
             assert f >= rows * 256 + rows * 2 * 4 and f >= last
             last = f
             a, b = (lib.moe_forward_fp8_workspace_bytes(ctypes.byref(L), T, 4, fl) for fl in (0, 16))
-            assert a > b >= f + T * 1024 + rows * 1024 * 2
+            assert a >= b >= f + T * 1024
+            if T * 4 > 64:   # the per-pair outputs pass through the workspace
+                assert a > b >= f + T * 1024 + rows * 1024 * 2
     assert lib.moe_forward_fp8_workspace_bytes(ctypes.byref(L), 1, 4, 2) == 0
     assert lib.moe_forward_fp8_workspace_bytes(None, 1, 4, 0) == 0 and lib.moe_ffn_fp8_workspace_bytes(ctypes.byref(L), 0, 4) == 0
 
@@ -157,21 +159,21 @@ def test_binding_checks_tensors_before_the_call():
     for bad, msg in [
         (lambda: qm.Fp8Matrix(torch.zeros(1, 8, 16), torch.zeros(1, 1, 1)), "e4m3 codes"),
         (lambda: qm.Fp8Matrix(torch.zeros(8, 16, dtype=torch.uint8), torch.zeros(1, 1, 1)), "rows"),
-        (lambda: qm.Fp8Matrix(torch.zeros(1, 8, 16, dtype=torch.uint8), torch.zeros(1, 1, 2)), "scale has shape"),
+        (lambda: qm.Fp8Matrix(torch.zeros(1, 8, 16, dtype=torch.uint8), torch.zeros(1, 1, 2)), "scale: "),
         (lambda: qm.Fp8Matrix(torch.zeros(1, 16, 8, dtype=torch.uint8).transpose(1, 2), torch.zeros(1, 1, 1)), "columns"),
-        (lambda: qm.moe_quantize_fp8(x, f8[:3], d), "xq has shape"),
+        (lambda: qm.moe_quantize_fp8(x, f8[:3], d), "xq: "),
         (lambda: qm.moe_quantize_fp8(x, x, d), "e4m3 codes"),
         (lambda: qm.moe_quantize_fp8(x.t(), f8.t(), d), "columns"),
-        (lambda: qm.moe_quantize_fp8(x, f8, d.int()), "dtype"),
+        (lambda: qm.moe_quantize_fp8(x, f8, d.int()), "xs: "),
         (lambda: qm.moe_quantize_fp8(x.double(), f8, d), "dtype"),
         (lambda: qm.moe_quantize_fp8(x, f8, d), "on a GPU"),
-        (lambda: qm.moe_matmul_fp8(f8[:, :128].contiguous(), d, w, y), "xq has shape"),
-        (lambda: qm.moe_matmul_fp8(f8, d[:, :1], w, y), "xs has shape"),
+        (lambda: qm.moe_matmul_fp8(f8[:, :128].contiguous(), d, w, y), "xq: "),
+        (lambda: qm.moe_matmul_fp8(f8, d[:, :1], w, y), "xs: "),
         (lambda: qm.moe_matmul_fp8(f8, d, w, y[:, :255]), "y has shape"),
         (lambda: qm.moe_matmul_fp8(f8, d, w, y.t().contiguous().t()), "contiguous columns"),
         (lambda: qm.moe_matmul_fp8(f8, d, w, y.int()), "dtype"),
         (lambda: qm.RouteSpec("relu"), "score"),
-        (lambda: qm.RouteSpec(bias=torch.zeros(8, dtype=torch.float64)), "dtype"),
+        (lambda: qm.RouteSpec(bias=torch.zeros(8, dtype=torch.float64)), "bias: "),
         (lambda: qm.Fp8Layer(w, w, w, (w, w)), "shared"),
     ]:
         with pytest.raises(ValueError, match=msg):
@@ -180,7 +182,7 @@ def test_binding_checks_tensors_before_the_call():
     lg = torch.zeros(4, 8)
     for bad, msg in [
         (lambda: qm.moe_route_scored(lg, 3, r, qm.RouteSpec()), "routing buffers"),
-        (lambda: qm.moe_route_scored(lg.half(), 2, r, qm.RouteSpec()), "dtype"),
+        (lambda: qm.moe_route_scored(lg.half(), 2, r, qm.RouteSpec()), "logits: "),
         (lambda: qm.moe_route_scored(lg, 2, r, qm.RouteSpec(bias=torch.zeros(7))), "bias has 7"),
         (lambda: qm.moe_route_scored(lg, 2, r, qm.RouteSpec()), "on a GPU"),
     ]:
