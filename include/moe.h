@@ -417,7 +417,7 @@ moe_status moe_quantize_fp8(const void* x, int32_t x_type, int64_t ldx, int32_t 
  * xq [T][K] and xs [T][ceil(K/128)] from moe_quantize_fp8 (K = w->cols), w one
  * matrix (N = w->rows); y [T][N] of y_type, rows ldy elements apart.  The sum
  * over b is fp32, y is rounded once.  For an fp32 y the block products are
- * summed in fp32 too; for bf16 and fp16 the 8-bit matrix unit forms them, which
+ * summed in fp32 too; for bf16 and fp16 the 8-bit matrix unit may form them, which
  * drops bits below 2^-13 of the largest of each eight consecutive products
  * (their sum is off by at most 7 * 2^-13 of it).  A row of y depends
  * on its own row of xq and xs only, but the order of its fp32 sum follows

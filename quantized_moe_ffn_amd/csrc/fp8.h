@@ -139,6 +139,36 @@ typedef float v4f_f8 __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h_f8 __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h_f8 __attribute__((ext_vector_type(2)));
 
+// Sixteen bytes of zeros: the source of copies past a row's last column.
+__device__ __attribute__((aligned(16))) const uint32_t g_fp8_zero[4] = {0, 0, 0, 0};
+
+// One asynchronous copy instruction of a wave: lane l's 16 (or
+// 4) bytes at src go to LDS byte lds + 16*l (or 4*l).  lds is wave-uniform.
+// The compiler does not count these loads (with its own builtin it waits for
+// all of them before any LDS read, which leaves no stage in flight); the
+// kernels wait on vmcnt themselves.  No output register is written, and the
+// kernels hold nothing in m0.
+__device__ __forceinline__ void copy16_lds(const void* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
+}
+__device__ __forceinline__ void copy4_lds(const void* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// All of this wave's LDS reads are in registers, then the workgroup meets.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
 // The block product of one 16-row and one 16-token fragment (32 codes of a
 // row or token per lane, the same columns in both).
 template <bool EXACT>

@@ -37,32 +37,7 @@ namespace moe {
 
 namespace {
 
-__device__ __attribute__((aligned(16))) const uint32_t g_fp8_zero[4] = {0, 0, 0, 0};
-
 enum Fp8Mode { kFp8Dense, kFp8GateUp, kFp8Down };
-
-// One workgroup-wide asynchronous copy instruction of a wave: lane l's 16 (or
-// 4) bytes at src go to LDS byte lds + 16*l (or 4*l).  lds is wave-uniform.
-// The compiler does not count these loads (with its own builtin it waits for
-// all of them before any LDS read, which leaves no stage in flight); the
-// kernels wait on vmcnt themselves.  No output register is written, and the
-// kernels hold nothing in m0.
-__device__ __forceinline__ void copy16_lds(const void* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
-}
-__device__ __forceinline__ void copy4_lds(const void* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-// All of this wave's LDS reads are in registers, then the workgroup meets.
-__device__ __forceinline__ void lds_barrier() {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
 
 struct Fp8TileArgs {
     Fp8Mat w0, w1;             // dense: w0; gate/up: gate, up; down: w0
@@ -235,7 +210,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
     const int seg = C::MT >= 64 ? wave % (C::MT / 64) : 0;
     const float* ps = a.xs + src_row((C::MT >= 64 ? seg * 64 : 0) + lane) * KB;
 
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds;
+    const uint32_t lds0 = lds_address(lds);
     auto issue = [&](int kb) {
         const uint32_t st = lds0 + (kb % STAGES) * C::kStage;
         const uint32_t la = st + wave * 1024, lb = la + C::NR * 128;
@@ -416,8 +391,7 @@ hipError_t launch_grouped(const Fp8TileArgs& a, int64_t n_work, hipStream_t s) {
 
 template <bool EXACT>
 hipError_t launch_dense(const Fp8TileArgs& a, int mt, int64_t n_work, hipStream_t s) {
-    if (mt == 32) return launch_tile<kFp8Dense, EXACT, 4, 1, 4, 2, 2>(a, n_work, s);
-    if (mt == 64) return launch_tile<kFp8Dense, EXACT, 4, 2, 4, 2, 3>(a, n_work, s);
+    if (mt == 64) return launch_tile<kFp8Dense, EXACT, 2, 2, 2, 2, 4>(a, n_work, s);
     if (mt == 128) return launch_tile<kFp8Dense, EXACT, 4, 2, 4, 4, 3>(a, n_work, s);
     return launch_tile<kFp8Dense, false, 4, 2, 4, 8, 2>(a, n_work, s);
 }
@@ -477,7 +451,7 @@ hipError_t launch_ffn_fp8(const Fp8FfnArgs& f, hipStream_t s) {
 }
 
 hipError_t launch_matmul_fp8(const Fp8MatmulArgs& m, hipStream_t s) {
-    if (m.T <= 32 || (int64_t)((m.w.rows + 255) / 256) * ((m.T + 127) / 128) < 64) return launch_skinny_matmul(m, s);
+    if (m.T <= 32) return launch_skinny_matmul(m, s);
     Fp8TileArgs a{};
     a.w0 = m.w;
     a.xq = m.xq;
@@ -490,9 +464,11 @@ hipError_t launch_matmul_fp8(const Fp8MatmulArgs& m, hipStream_t s) {
     a.ldy = m.ldy;
     const int sz = m.yt == ElemType::kF32 ? 4 : 2;
     a.vec_ok = m.ldy % 4 == 0 && (uintptr_t)m.y % (4 * sz) == 0;
-    a.nblocks = (m.w.rows + 255) / 256;
     const bool exact = m.yt == ElemType::kF32;
-    const int mt = m.T <= 32 ? 32 : (m.T <= 64 ? 64 : (m.T <= 512 || exact ? 128 : 256));
+    // the largest tile that gives the chip's 256 CUs work: 64 x 64, 256 x 128 or 256 x 256 (rows x tokens)
+    const int64_t big = (m.w.rows + 255) / 256;
+    const int mt = big * ((m.T + 127) / 128) < 128 ? 64 : (exact || big * ((m.T + 255) / 256) < 128 ? 128 : 256);
+    a.nblocks = mt == 64 ? (m.w.rows + 63) / 64 : (int)big;
     a.n_mt = (m.T + mt - 1) / mt;
     const int64_t n_work = (int64_t)a.nblocks * a.n_mt;
     return exact ? launch_dense<true>(a, mt, n_work, s) : launch_dense<false>(a, mt, n_work, s);
