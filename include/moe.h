@@ -376,8 +376,8 @@ enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 30 };
 /* n_experts matrices of rows x cols e4m3 codes (one byte each, cols
  * contiguous, rows row_stride bytes and experts expert_stride bytes apart), one
  * fp32 scale per 128 x 128 block: scale [n_experts][ceil(rows/128)][ceil(cols/128)],
- * contiguous; w = scale * code.  cols a multiple of 16; data, row_stride and
- * expert_stride multiples of 16 bytes; scale 4-byte aligned. */
+ * contiguous; w = scale * code.  cols a multiple of 16; data, row_stride (at
+ * most 2^23) and expert_stride multiples of 16 bytes; scale 4-byte aligned. */
 typedef struct moe_fp8_matrix {
     const void* data;
     const float* scale;
@@ -435,7 +435,7 @@ size_t moe_ffn_fp8_workspace_bytes(const moe_fp8_layer* L, int32_t T, int32_t k)
  * every product as in moe_matmul_fp8 with an fp32 y.  xq, xs from moe_quantize_fp8; y_pair fp32
  * [T*k][H]; y_shared fp32 [T][H] (required iff has_shared); both 16-byte
  * aligned.  r as in moe_expert_ffn_q, from moe_route_topk or moe_route_scored
- * for the same T, k and E.  Workspace 256-byte aligned. */
+ * for the same T, k and E.  T*H below 2^32.  Workspace 256-byte aligned. */
 moe_status moe_expert_ffn_fp8(const moe_fp8_layer* L, const moe_routing* r, int32_t T, int32_t k, const void* xq,
                               const float* xs, float* y_pair, float* y_shared, void* workspace, size_t ws_bytes,
                               hipStream_t stream);

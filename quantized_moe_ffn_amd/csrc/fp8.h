@@ -154,6 +154,17 @@ __device__ __forceinline__ void copy16_lds(const void* src, uint32_t lds) {
 __device__ __forceinline__ void copy4_lds(const void* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory");
 }
+__device__ __forceinline__ uint64_t wave_uniform(uint64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (uint64_t)hi << 32 | lo;
+}
+// The same from a wave-uniform base and a 32-bit offset per lane.
+__device__ __forceinline__ void copy16_lds(uint64_t base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void copy4_lds(uint64_t base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void wait_vm() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
@@ -169,8 +180,9 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
-// The block product of one 16-row and one 16-token fragment (32 codes of a
-// row or token per lane, the same columns in both).
+// The block product of one 16-row and one 16-token fragment: lane 16*g + r holds
+// columns 16*g .. and 64 + 16*g .. (16 codes each) of row or token r, the same
+// columns in both operands, so the MFMA's own column order does not matter.
 template <bool EXACT>
 struct Fp8Frag;
 

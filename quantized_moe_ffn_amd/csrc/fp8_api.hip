@@ -61,7 +61,7 @@ moe_status check_fp8(const moe_fp8_matrix& m, const char* name, int rows, int co
     if (m.row_stride < m.cols || m.row_stride % 16)
         return fail(MOE_ERR_INVALID_ARGUMENT, "%s.row_stride = %lld: need a multiple of 16, at least cols = %d", name,
                     (long long)m.row_stride, m.cols);
-    if (m.row_stride > ((int64_t)1 << 40) / m.rows)
+    if (m.row_stride > (int64_t)1 << 23)   // 32-bit offsets inside a tile of 256 rows
         return fail(MOE_ERR_INVALID_ARGUMENT, "%s.row_stride = %lld is too large", name, (long long)m.row_stride);
     if (m.expert_stride % 16 ||
         (n_experts > 1 && m.expert_stride < (int64_t)(m.rows - 1) * m.row_stride + m.cols))
@@ -90,6 +90,8 @@ moe_status check_fp8_layer(const moe_fp8_layer* L, int T, int k) {
         return fail(MOE_ERR_INVALID_ARGUMENT, "k = %d: need 1 <= k <= min(E = %d, %d)", k, E, kMaxTopK);
     if ((int64_t)T * k > (int64_t)1 << 30)
         return fail(MOE_ERR_INVALID_ARGUMENT, "T*k = %lld is too large", (long long)T * k);
+    if ((int64_t)T * H >= (int64_t)1 << 32)   // 32-bit offsets of gathered rows
+        return fail(MOE_ERR_INVALID_ARGUMENT, "T*hidden = %lld: need less than 2^32", (long long)T * H);
     moe_status st;
     if ((st = check_fp8(L->gate, "gate", I, H, E)) != MOE_OK) return st;
     if ((st = check_fp8(L->up, "up", I, H, E)) != MOE_OK) return st;

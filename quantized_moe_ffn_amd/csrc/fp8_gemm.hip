@@ -24,8 +24,11 @@
 // Tiles.  A workgroup takes NR weight rows x MT tokens; both operands pass
 // through LDS in 128-byte (one block deep) row slices, loaded straight from
 // global memory (global_load_lds_dwordx4: no registers, no ds_write), STAGES
-// deep.  A row's eight 16-byte chunks are stored at chunk ^ (row & 7), so the
-// eight rows a ds_read_b128 phase touches fall on different banks.
+// deep.  A row's eight 16-byte chunks are stored at chunk ^ (row & 7) and a lane
+// reads chunks g and g + 4 (g = lane/16): the sixteen lanes of a ds_read_b128
+// phase (0-3, 12-15, 20-23, 24-27 and so on) then cover all 64 banks.  With
+// chunks 2g and 2g + 1 every phase took two turns (SQ_LDS_BANK_CONFLICT 46% of
+// the LDS cycles).
 //
 // Grouped modes: gate/up interleaves 16-row tiles of gate and up in one wave,
 // so SiLU(gate)*up is formed in registers, and its 128 rows of I are one scale
@@ -90,7 +93,7 @@ __device__ __forceinline__ void store4(void* base, int64_t idx, ElemType t, cons
     }
 }
 
-template <int NWN, int NWM, int WN, int WM, int STAGES>
+template <bool PP, int NWN, int NWM, int WN, int WM, int STAGES>
 struct Fp8Tile {
     static constexpr int kWaves = NWN * NWM;
     static constexpr int kThreads = kWaves * kWave;
@@ -98,17 +101,22 @@ struct Fp8Tile {
     static constexpr int MT = NWM * WM * 16;
     static constexpr int NA = NR / 8 / kWaves;   // weight copies of a wave per stage
     static constexpr int NB = MT / 8 / kWaves;   // token copies
-    static constexpr int kLoads = NA + NB + 1;   // + the token scales
-    static constexpr int kScaleFloats = MT < 64 ? 64 : MT;
-    static constexpr int kStage = (NR + MT) * 128 + kScaleFloats * 4;
-    static constexpr int kLds = STAGES * kStage;
+    // Token scales.  One copy a stage and wave (tokens in [stage][64 or MT] words) gathers
+    // a line per token for four bytes of it: as many line reads as the codes themselves.
+    // The ping-pong tiles, whose K is a multiple of four blocks, copy sixteen bytes of
+    // each token every fourth stage instead, into two buffers of [MT][4] words.
+    static constexpr int kSegs = MT < 64 ? 1 : MT / 64;   // copies that hold all tokens
+    static constexpr int kLoads = NA + NB + (PP ? 0 : 1); // copies of a wave in every stage
+    static constexpr int kStage = (NR + MT) * 128 + (PP ? 0 : (kSegs + 1) * 256);
+    static constexpr int kRing = STAGES * kStage;
+    static constexpr int kLds = kRing + (PP ? 2 * MT * 16 : 0);
     static_assert(NA * 8 * kWaves == NR && NB * 8 * kWaves == MT, "copies divide evenly");
-    static_assert(kLds <= 160 * 1024, "LDS");
+    static_assert(kSegs <= kWaves && kLds <= 160 * 1024, "scale copies, LDS");
 };
 
-template <int MODE, bool EXACT, int NWN, int NWM, int WN, int WM, int STAGES>
+template <int MODE, bool EXACT, bool PP, int NWN, int NWM, int WN, int WM, int STAGES>
 __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8TileArgs a) {
-    using C = Fp8Tile<NWN, NWM, WN, WM, STAGES>;
+    using C = Fp8Tile<PP, NWN, NWM, WN, WM, STAGES>;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     __shared__ int s_row[C::MT];                 // output row of each token of the tile, -1: none
     __shared__ uint32_t s_amax[MODE == kFp8GateUp ? NWN : 1][C::MT];
@@ -134,22 +142,22 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
         mt0 = (in / width) * C::MT;
         n_tok = min(C::MT, a.T - mt0);
     } else {
-        const int n_work = *a.tl.n_tiles * a.nblocks;
+        const int n_work = __builtin_amdgcn_readfirstlane(*a.tl.n_tiles) * a.nblocks;
         const int chunk = (n_work + 7) / 8;
         const int w = (blockIdx.x % 8) * chunk + blockIdx.x / 8;
         if ((int)(blockIdx.x / 8) >= chunk || w >= n_work) return;
         const int u = w / a.nblocks;
         nb = w - u * a.nblocks;
-        e = a.tl.tile_e[u];
-        mt0 = a.tl.tile_m0[u];
+        e = __builtin_amdgcn_readfirstlane(a.tl.tile_e[u]);
+        mt0 = __builtin_amdgcn_readfirstlane(a.tl.tile_m0[u]);
         shared = e >= a.E;
         int c = a.T;
         if (shared) {
             m0 = a.s0;
             m1 = a.s1;
         } else {
-            c = a.count[e];
-            off = a.offset[e];
+            c = __builtin_amdgcn_readfirstlane(a.count[e]);
+            off = __builtin_amdgcn_readfirstlane(a.offset[e]);
             if (c < 0 || off < 0 || (int64_t)off + c > (int64_t)a.T * a.k) {   // buffers not from a routing pass
                 if (tid == 0) raise_error(kErrPairRange);
                 return;
@@ -176,60 +184,72 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
         __syncthreads();
         if (n_tok <= 0) return;
     }
-    // source row of tile token m (a clamped valid row past the end)
-    auto src_row = [&](int m) -> int64_t {
+    // copy sources: lane l of copy i holds row 8*(copy) + l/8, chunk (l%8) ^ (row%8), as a 32-bit offset from a
+    // wave-uniform base (the host bounds row_stride and T*K)
+    const int lr = lane >> 3;
+    const int ca = ((lane & 7) ^ lr) * 16;   // the chunk's first column within a block (rows advance by multiples of 8)
+    uint64_t ba[C::NA];
+    uint32_t oa[C::NA], ob[C::NB];
+#pragma unroll
+    for (int i = 0; i < C::NA; ++i) {
+        const int R8 = (wave + i * C::kWaves) * 8;   // the copy's first row in the tile
+        if constexpr (MODE == kFp8GateUp) {
+            const int w_ = R8 / (WN * 16), t_ = (R8 / 16) % WN, r_ = R8 & 15;
+            const int row = nb * (C::NR / 2) + w_ * (WN / 2 * 16) + (t_ % (WN / 2)) * 16 + r_;
+            const Fp8Mat& m = t_ < WN / 2 ? m0 : m1;
+            ba[i] = wave_uniform((uint64_t)(m.data + (int64_t)row * m.row_stride));
+            oa[i] = (uint32_t)(lr * (int)m.row_stride + ca);
+        } else {
+            const int first = min(nb * C::NR, a.N - 1);
+            ba[i] = wave_uniform((uint64_t)(m0.data + (int64_t)first * m0.row_stride));
+            oa[i] = (uint32_t)((min(nb * C::NR + R8 + lr, a.N - 1) - first) * (int)m0.row_stride + ca);
+        }
+    }
+    const int64_t tok0 = MODE == kFp8Dense ? mt0 : (MODE == kFp8Down ? (shared ? (int64_t)a.T * a.k : (int64_t)off) + mt0 : 0);
+    const uint64_t bb = wave_uniform((uint64_t)(a.xq + tok0 * K));
+    // token of the tile's row m from tok0 on (a valid one past the end)
+    auto src_row = [&](int m) -> uint32_t {
         m = min(m, n_tok - 1);
-        if constexpr (MODE == kFp8Dense) return mt0 + m;
-        if constexpr (MODE == kFp8Down) return (shared ? (int64_t)a.T * a.k : (int64_t)off) + mt0 + m;
+        if constexpr (MODE != kFp8GateUp) return m;
         const int row = s_row[m];
         return shared ? row : max(row, 0) / a.k;
     };
-
-    // copy sources: lane l of copy i holds row 8*(copy) + l/8, chunk (l%8) ^ (row%8)
-    const uint8_t* pa[C::NA];
-    const uint8_t* pb[C::NB];
-    const int lr = lane >> 3;
-    const int ca = ((lane & 7) ^ lr) * 16;   // the chunk's first column within a block (rows advance by multiples of 8)
 #pragma unroll
-    for (int i = 0; i < C::NA; ++i) {
-        const int R = (wave + i * C::kWaves) * 8 + lr;
-        if constexpr (MODE == kFp8GateUp) {
-            const int w_ = R / (WN * 16), t_ = (R / 16) % WN, r_ = R & 15;
-            const int row = nb * (C::NR / 2) + w_ * (WN / 2 * 16) + (t_ % (WN / 2)) * 16 + r_;
-            const Fp8Mat& m = t_ < WN / 2 ? m0 : m1;
-            pa[i] = m.data + (int64_t)row * m.row_stride + ca;
-        } else {
-            pa[i] = m0.data + (int64_t)min(nb * C::NR + R, a.N - 1) * m0.row_stride + ca;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < C::NB; ++i) {
-        const int R = (wave + i * C::kWaves) * 8 + lr;
-        pb[i] = a.xq + src_row(R) * K + ca;
-    }
-    const int seg = C::MT >= 64 ? wave % (C::MT / 64) : 0;
-    const float* ps = a.xs + src_row((C::MT >= 64 ? seg * 64 : 0) + lane) * KB;
+    for (int i = 0; i < C::NB; ++i) ob[i] = src_row((wave + i * C::kWaves) * 8 + lr) * (uint32_t)K + ca;
+    // token scales: waves below kSegs copy 64 tokens each; without ping-pong the others copy one word to a
+    // spare place, so that every wave has the same copies in flight
+    const int seg = PP ? wave % C::kSegs : min(wave, C::kSegs);
+    const uint64_t bs = wave_uniform((uint64_t)(a.xs + tok0 * KB));
+    const uint32_t os = !PP && wave >= C::kSegs ? 0u : src_row(seg * 64 + lane) * (uint32_t)KB * 4;
 
     const uint32_t lds0 = lds_address(lds);
     auto issue = [&](int kb) {
         const uint32_t st = lds0 + (kb % STAGES) * C::kStage;
         const uint32_t la = st + wave * 1024, lb = la + C::NR * 128;
-        if ((kb + 1) * kFp8Block <= K) {
+        const uint64_t o = (uint64_t)kb * kFp8Block;
+        if (PP || (kb + 1) * kFp8Block <= K) {   // ping-pong tiles are launched for multiples of four blocks only
 #pragma unroll
-            for (int i = 0; i < C::NA; ++i) copy16_lds(pa[i] + kb * kFp8Block, la + i * C::kWaves * 1024);
+            for (int i = 0; i < C::NA; ++i) copy16_lds(ba[i] + o, oa[i], la + i * C::kWaves * 1024);
 #pragma unroll
-            for (int i = 0; i < C::NB; ++i) copy16_lds(pb[i] + kb * kFp8Block, lb + i * C::kWaves * 1024);
+            for (int i = 0; i < C::NB; ++i) copy16_lds(bb + o, ob[i], lb + i * C::kWaves * 1024);
         } else {   // the last block of a K that is no multiple of 128: chunks past the last column read zeros
-            const bool live = kb * kFp8Block + ca < K;
-            const uintptr_t z = (uintptr_t)g_fp8_zero;
+            int col = (int)o + ca;
+            asm volatile("" : "+v"(col));   // keeps the addresses of this path out of the loop's registers
+            const bool live = col < K;
+            const uint64_t z = (uint64_t)g_fp8_zero;
+            const int64_t d = col - ca;
 #pragma unroll
             for (int i = 0; i < C::NA; ++i)
-                copy16_lds((const void*)(live ? (uintptr_t)(pa[i] + kb * kFp8Block) : z), la + i * C::kWaves * 1024);
+                copy16_lds((const void*)(live ? ba[i] + (d + oa[i]) : z), la + i * C::kWaves * 1024);
 #pragma unroll
             for (int i = 0; i < C::NB; ++i)
-                copy16_lds((const void*)(live ? (uintptr_t)(pb[i] + kb * kFp8Block) : z), lb + i * C::kWaves * 1024);
+                copy16_lds((const void*)(live ? bb + (d + ob[i]) : z), lb + i * C::kWaves * 1024);
         }
-        copy4_lds(ps + kb, st + (C::NR + C::MT) * 128 + seg * 256);
+        if constexpr (PP) {
+            if ((kb & 3) == 0) copy16_lds(bs + 4 * (uint64_t)kb, os, lds0 + C::kRing + ((kb >> 2) & 1) * C::MT * 16 + seg * 1024);
+        } else {
+            copy4_lds(bs + 4 * (uint64_t)kb, os, st + (C::NR + C::MT) * 128 + seg * 256);
+        }
     };
 
     // this wave's weight scales: lane l holds block l of a group of 64 blocks
@@ -241,50 +261,162 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
 
     v4f_f8 acc[WN][WM] = {};
     const int g = lane >> 4, r16 = lane & 15;
-    const int c0 = ((2 * g) ^ (r16 & 7)) * 16, c1 = ((2 * g + 1) ^ (r16 & 7)) * 16;
+    const int c0 = (g ^ (r16 & 7)) * 16, c1 = c0 ^ 64;   // chunks g and g + 4
 
+    // this lane's fragment addresses in stage 0: 16 rows are 2,048 bytes, so tile i is an immediate away
+    const unsigned char* la0 = lds + (wn * WN * 16 + r16) * 128 + c0;
+    const unsigned char* la1 = lds + (wn * WN * 16 + r16) * 128 + c1;
+    const unsigned char* lb0 = lds + C::NR * 128 + (wm * WM * 16 + r16) * 128 + c0;
+    const unsigned char* lb1 = lds + C::NR * 128 + (wm * WM * 16 + r16) * 128 + c1;
+    constexpr int kXs = PP ? 16 : 4;   // bytes from one token's scale to the next
+    const unsigned char* lsx = lds + (PP ? C::kRing : (C::NR + C::MT) * 128) + (wm * WM * 16 + r16) * kXs;
+    auto load_a = [&](Fp8Frag<EXACT>(&fa)[WN], int st) {
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        if (s < KB) issue(s);
-    for (int kb = 0; kb < KB; ++kb) {
-        if ((kb & 63) == 0 && kb > 0) {   // the compiler waits on these (and so on every older copy) at their use
-            ws0 = w0s[min(kb + lane, KB - 1)];
-            if constexpr (MODE == kFp8GateUp) ws1 = w1s[min(kb + lane, KB - 1)];
-        }
-        if (kb + STAGES - 2 < KB)
-            wait_vm<(STAGES - 2) * C::kLoads>();
-        else
-            wait_vm<0>();
-        lds_barrier();
-        if (kb + STAGES - 1 < KB) issue(kb + STAGES - 1);
-        const unsigned char* st = lds + (kb % STAGES) * C::kStage;
-        const float wb0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ws0), kb & 63));
-        const float wb1 = MODE == kFp8GateUp
-                              ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ws1), kb & 63))
-                              : 0.f;
-        Fp8Frag<EXACT> fa[WN];
+        for (int i = 0; i < WN; ++i)
+            fa[i].set(*reinterpret_cast<const int4*>(la0 + st + i * 2048), *reinterpret_cast<const int4*>(la1 + st + i * 2048));
+    };
+    auto load_b = [&](Fp8Frag<EXACT>& fb, float& x, int st, int sx, int j) {
+        fb.set(*reinterpret_cast<const int4*>(lb0 + st + j * 2048), *reinterpret_cast<const int4*>(lb1 + st + j * 2048));
+        x = *reinterpret_cast<const float*>(lsx + sx + j * 16 * kXs);
+    };
+    auto add_tile = [&](const Fp8Frag<EXACT>(&fa)[WN], const Fp8Frag<EXACT>& fb, float x, float wb0, float wb1, int j) {
+        const float s0 = x * wb0, s1 = MODE == kFp8GateUp ? x * wb1 : 0.f;
 #pragma unroll
         for (int i = 0; i < WN; ++i) {
-            const unsigned char* p = st + ((wn * WN + i) * 16 + r16) * 128;
-            fa[i].set(*reinterpret_cast<const int4*>(p + c0), *reinterpret_cast<const int4*>(p + c1));
+            const v4f_f8 t = fa[i].times(fb);
+            const float s = MODE == kFp8GateUp && i >= WN / 2 ? s1 : s0;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(t[v], s, acc[i][j][v]);
         }
-        const float* sx = reinterpret_cast<const float*>(st + (C::NR + C::MT) * 128);
+    };
+    auto block_scales = [&](int kb, float& wb0, float& wb1) {
+        wb0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ws0), kb & 63));
+        wb1 = MODE == kFp8GateUp ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ws1), kb & 63)) : 0.f;
+        if ((kb & 63) == 63) {   // the compiler waits on these (and so on every older copy) at their use
+            ws0 = w0s[min(kb + 1 + lane, KB - 1)];
+            if constexpr (MODE == kFp8GateUp) ws1 = w1s[min(kb + 1 + lane, KB - 1)];
+        }
+    };
+    if constexpr (!PP) {
 #pragma unroll
-        for (int j = 0; j < WM; ++j) {
-            const int m = (wm * WM + j) * 16 + r16;
-            const unsigned char* p = st + C::NR * 128 + m * 128;
-            Fp8Frag<EXACT> fb;
-            fb.set(*reinterpret_cast<const int4*>(p + c0), *reinterpret_cast<const int4*>(p + c1));
-            const float x = sx[m];
-            const float s0 = x * wb0, s1 = MODE == kFp8GateUp ? x * wb1 : 0.f;
+        for (int s = 0; s < STAGES - 1; ++s)
+            if (s < KB) issue(s);
+        int st = 0;
+        for (int kb = 0; kb < KB; ++kb) {
+            float wb0, wb1;
+            block_scales(kb, wb0, wb1);
+            if (kb + STAGES - 2 < KB)
+                wait_vm<(STAGES - 2) * C::kLoads>();
+            else
+                wait_vm<0>();
+            lds_barrier();
+            if (kb + STAGES - 1 < KB) issue(kb + STAGES - 1);
+            Fp8Frag<EXACT> fa[WN];
+            load_a(fa, st);
 #pragma unroll
-            for (int i = 0; i < WN; ++i) {
-                const v4f_f8 t = fa[i].times(fb);
-                const float s = MODE == kFp8GateUp && i >= WN / 2 ? s1 : s0;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(t[v], s, acc[i][j][v]);
+            for (int j = 0; j < WM; ++j) {
+                Fp8Frag<EXACT> fb;
+                float x;
+                load_b(fb, x, st, st, j);
+                add_tile(fa, fb, x, wb0, wb1, j);
             }
+            st = st + C::kStage == C::kRing ? 0 : st + C::kStage;
         }
+    } else {
+        // Two groups of four waves (one of each on every SIMD) alternate: while one
+        // reads its fragments from LDS, the other runs MFMAs on those it holds.  A
+        // half step ends at a barrier; group 1 runs one half step behind.  Stage s is
+        // last read one half step before group 0 starts on stage s + 1, so its buffer
+        // takes stage s + STAGES from there on: group 0 issues it as it starts to read
+        // stage s + 1, group 1 as it computes its last part of stage s.
+        constexpr int TB = EXACT ? 2 : 4, PH = WM / TB;
+        static_assert(WM % TB == 0 && NWM == 2 && (C::NR + C::MT) % kWave == 0, "ping-pong shape");
+        const int grp = wm;
+        auto meet = [&]() {
+            __builtin_amdgcn_sched_barrier(0);
+            lds_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // this wave's copies of stage s; up to STAGES - 2 newer stages are in flight
+        auto landed = [&](int s) {
+            if (s >= KB) return;
+            if (s + STAGES - 2 < KB)
+                wait_vm<(STAGES - 2) * C::kLoads>();
+            else
+                wait_vm<0>();
+        };
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s)
+            if (s < KB) issue(s);
+        if (grp == 0) {
+            landed(0);
+        } else if (STAGES - 1 < KB) {   // group 1 issues a stage half a step before group 0 does
+            issue(STAGES - 1);
+            wait_vm<(STAGES - 1) * C::kLoads>();
+        } else {
+            wait_vm<0>();
+        }
+        meet();
+        if (grp == 1) meet();
+        int st = 0;
+        Fp8Frag<EXACT> fa[WN];
+        for (int kb = 0; kb < KB; ++kb) {
+            float wb0, wb1;
+            block_scales(kb, wb0, wb1);
+#pragma unroll
+            for (int ph = 0; ph < PH; ++ph) {
+                if (ph == 0 && grp == 0 && kb + STAGES - 1 < KB) issue(kb + STAGES - 1);
+                Fp8Frag<EXACT> fb[TB];
+                float s0[TB], s1[TB];
+                if (ph == 0) load_a(fa, st);
+#pragma unroll
+                for (int j = 0; j < TB; ++j) {
+                    float x;
+                    load_b(fb[j], x, st, ((kb >> 2) & 1) * C::MT * 16 + (kb & 3) * 4, ph * TB + j);
+                    s0[j] = x * wb0;
+                    s1[j] = MODE == kFp8GateUp ? x * wb1 : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < TB; ++j) asm volatile("" : "+v"(s0[j]), "+v"(s1[j]));   // in this half step
+                if (ph == PH - 1 && grp == 1) landed(kb + 1);
+                meet();
+                if (ph == PH - 1 && grp == 1 && kb + STAGES < KB) issue(kb + STAGES);
+                __builtin_amdgcn_s_setprio(1);
+                // tile q's MFMA goes out two tiles before its product is added, so the adds never wait on it
+                constexpr int Q = TB * WN;
+                v4f_f8 t[Q];
+                auto add = [&](int q) {
+                    const int i = q % WN, j = q / WN;
+                    const float s = MODE == kFp8GateUp && i >= WN / 2 ? s1[j] : s0[j];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[i][ph * TB + j][v] = fmaf(t[q][v], s, acc[i][ph * TB + j][v]);
+                };
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    t[q] = fa[q % WN].times(fb[q / WN]);
+                    if (q >= 2) add(q - 2);
+                }
+                add(Q - 2);
+                add(Q - 1);
+                constexpr int kM = EXACT ? 4 : 1;   // MFMAs of a tile
+                __builtin_amdgcn_sched_group_barrier(0x8, 2 * kM, 0);
+#pragma unroll
+                for (int q = 2; q < Q; ++q) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, kM, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+                }
+                // the sums belong to this half step: pure arithmetic would otherwise drift past its barrier
+#pragma unroll
+                for (int j = 0; j < TB; ++j)
+#pragma unroll
+                    for (int i = 0; i < WN; ++i) asm volatile("" : "+v"(acc[i][ph * TB + j]));
+                __builtin_amdgcn_s_setprio(0);
+                if (ph == PH - 1 && grp == 0) landed(kb + 1);
+                meet();
+            }
+            st = st + C::kStage == C::kRing ? 0 : st + C::kStage;
+        }
+        if (grp == 0) meet();
     }
 
     // value v of acc[i][j]: weight row 16*i + 4*g + v of the wave, token 16*j + r16 of the wave
@@ -363,11 +495,11 @@ __global__ void __launch_bounds__(1024) fp8_tiles_kernel(const int32_t* count, i
     write_tile_list(tid < E ? count[tid] : 0, npairs, E, tl, s_wave, s_start);
 }
 
-template <int MODE, bool EXACT, int NWN, int NWM, int WN, int WM, int STAGES>
+template <int MODE, bool EXACT, bool PP, int NWN, int NWM, int WN, int WM, int STAGES>
 hipError_t launch_tile(const Fp8TileArgs& a, int64_t n_work, hipStream_t s) {
-    using C = Fp8Tile<NWN, NWM, WN, WM, STAGES>;
+    using C = Fp8Tile<PP, NWN, NWM, WN, WM, STAGES>;
     const unsigned grid = (unsigned)((n_work + 7) / 8 * 8);
-    fp8_tile_kernel<MODE, EXACT, NWN, NWM, WN, WM, STAGES><<<grid, C::kThreads, C::kLds, s>>>(a);
+    fp8_tile_kernel<MODE, EXACT, PP, NWN, NWM, WN, WM, STAGES><<<grid, C::kThreads, C::kLds, s>>>(a);
     return hipGetLastError();
 }
 
@@ -384,16 +516,18 @@ int fp8_max_tiles(int T, int k, int E, int has_shared, int mt) {
 
 template <int MODE, bool EXACT>
 hipError_t launch_grouped(const Fp8TileArgs& a, int64_t n_work, hipStream_t s) {
-    if (a.tl.mt == 32) return launch_tile<MODE, EXACT, 4, 1, 4, 2, 2>(a, n_work, s);
-    if (a.tl.mt == 64) return launch_tile<MODE, EXACT, 4, 2, 4, 2, 3>(a, n_work, s);
-    return launch_tile<MODE, EXACT, 4, 2, 4, 4, 3>(a, n_work, s);
+    if (a.tl.mt == 32) return launch_tile<MODE, EXACT, false, 4, 1, 4, 2, 2>(a, n_work, s);
+    if (a.tl.mt == 64) return launch_tile<MODE, EXACT, false, 4, 2, 4, 2, 3>(a, n_work, s);
+    if (a.K % (4 * kFp8Block)) return launch_tile<MODE, EXACT, false, 4, 2, 4, 4, 3>(a, n_work, s);
+    return launch_tile<MODE, EXACT, true, 4, 2, 4, 4, 3>(a, n_work, s);
 }
 
 template <bool EXACT>
 hipError_t launch_dense(const Fp8TileArgs& a, int mt, int64_t n_work, hipStream_t s) {
-    if (mt == 64) return launch_tile<kFp8Dense, EXACT, 2, 2, 2, 2, 4>(a, n_work, s);
-    if (mt == 128) return launch_tile<kFp8Dense, EXACT, 4, 2, 4, 4, 3>(a, n_work, s);
-    return launch_tile<kFp8Dense, false, 4, 2, 4, 8, 2>(a, n_work, s);
+    if (mt == 64) return launch_tile<kFp8Dense, EXACT, false, 2, 2, 2, 2, 4>(a, n_work, s);
+    if (mt == 128 && a.K % (4 * kFp8Block)) return launch_tile<kFp8Dense, EXACT, false, 4, 2, 4, 4, 3>(a, n_work, s);
+    if (mt == 128) return launch_tile<kFp8Dense, EXACT, true, 4, 2, 4, 4, 3>(a, n_work, s);
+    return launch_tile<kFp8Dense, false, true, 4, 2, 4, 8, 2>(a, n_work, s);
 }
 
 }  // namespace
@@ -467,7 +601,7 @@ hipError_t launch_matmul_fp8(const Fp8MatmulArgs& m, hipStream_t s) {
     const bool exact = m.yt == ElemType::kF32;
     // the largest tile that gives the chip's 256 CUs work: 64 x 64, 256 x 128 or 256 x 256 (rows x tokens)
     const int64_t big = (m.w.rows + 255) / 256;
-    const int mt = big * ((m.T + 127) / 128) < 128 ? 64 : (exact || big * ((m.T + 255) / 256) < 128 ? 128 : 256);
+    const int mt = big * ((m.T + 127) / 128) < 128 ? 64 : (exact || m.w.cols % (4 * kFp8Block) || big * ((m.T + 255) / 256) < 128 ? 128 : 256);
     a.nblocks = mt == 64 ? (m.w.rows + 63) / 64 : (int)big;
     a.n_mt = (m.T + mt - 1) / mt;
     const int64_t n_work = (int64_t)a.nblocks * a.n_mt;

@@ -53,7 +53,7 @@ struct SkinnyWave {
         const int lane = threadIdx.x & (kWave - 1), r16 = lane & 15, g = lane >> 4;
         const int KB = (K + kFp8Block - 1) / kFp8Block;
         const int n = kb0 < KB ? (KB - 1 - kb0) / step + 1 : 0;   // blocks of this wave
-        const int c0 = ((2 * g) ^ (r16 & 7)) * 16, c1 = ((2 * g + 1) ^ (r16 & 7)) * 16;
+        const int c0 = (g ^ (r16 & 7)) * 16, c1 = c0 ^ 64;
         const uintptr_t z = (uintptr_t)g_fp8_zero;
         auto issue = [&](int u) {
             const int kb = kb0 + u * step;
@@ -121,8 +121,8 @@ struct SkinnyWave {
                     Fp8Frag<EXACT> fb;
                     float x;
                     if constexpr (TT == 0) {
-                        const int4* p = reinterpret_cast<const int4*>(px + u * kFp8Block + g * 32);
-                        fb.set(p[0], p[1]);
+                        const int4* p = reinterpret_cast<const int4*>(px + u * kFp8Block + g * 16);
+                        fb.set(p[0], p[4]);
                         x = ps[RT * kSkinnyChunk + u];
                     } else {
                         const unsigned char* p = st + (RT + j) * 2048;
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kSkinnyThreads) skinny_down_kernel(const Fp8Ff
     const int KB = f.I / kFp8Block, P = f.T * f.k;
     const int slots = f.k + (f.has_shared ? 1 : 0);
     const int ca = ((lane & 7) ^ (lane >> 3)) * 16;
-    const int c0 = ((2 * g) ^ (r16 & 7)) * 16, c1 = ((2 * g + 1) ^ (r16 & 7)) * 16;
+    const int c0 = (g ^ (r16 & 7)) * 16, c1 = c0 ^ 64;
     const uint32_t l0 = lds_address(s_w[wave]);
     for (int j = wave; j < slots; j += kSkinnyWaves) {
         const bool shared = j == f.k;
@@ -329,11 +329,11 @@ __global__ void __launch_bounds__(kSkinnyThreads) skinny_down_kernel(const Fp8Ff
 #pragma unroll
             for (int u = 0; u < kCh; ++u) {
                 if (u >= n) break;
-                const int4* p = reinterpret_cast<const int4*>(&s_q[wave][u * kFp8Block + g * 32]);
+                const int4* p = reinterpret_cast<const int4*>(&s_q[wave][u * kFp8Block + g * 16]);
                 const unsigned char* a = s_w[wave] + u * 2048 + r16 * 128;
                 Fp8Frag<EXACT> fa, fb;
                 fa.set(*reinterpret_cast<const int4*>(a + c0), *reinterpret_cast<const int4*>(a + c1));
-                fb.set(p[0], p[1]);
+                fb.set(p[0], p[4]);
                 const v4f_f8 x = fa.times(fb);
                 const float s = d[u] * wv[u];
 #pragma unroll

@@ -78,7 +78,7 @@ def _mm(w=None, xq=4096, xs=4096, T=2, y=4096, yt=30, ldy=256):
     (dict(w=_mat(data=0)), 1, "data or scale is NULL"), (dict(w=_mat(scale=0)), 1, "data or scale is NULL"),
     (dict(w=_mat(rows=0)), 1, "0 x 512"), (dict(w=_mat(cols=8)), 1, "256 x 8"), (dict(w=_mat(cols=520)), 1, "multiple of 16"),
     (dict(w=_mat(row_stride=496)), 1, "row_stride = 496"), (dict(w=_mat(row_stride=520)), 1, "row_stride = 520"),
-    (dict(w=_mat(row_stride=1 << 40)), 1, "too large"), (dict(w=_mat(expert_stride=8)), 1, "expert_stride = 8"),
+    (dict(w=_mat(row_stride=(1 << 23) + 16)), 1, "too large"), (dict(w=_mat(expert_stride=8)), 1, "expert_stride = 8"),
     (dict(w=_mat(data=4104)), 1, "16-byte aligned"), (dict(ldy=255), 1, "ldy = 255"), (dict(xq=4104), 1, "xq must be 16-byte"),
     (dict(y=4097), 1, "element aligned"), (dict(y=4098, yt=0), 1, "element aligned"),
 ])
@@ -106,7 +106,7 @@ def _fwd(L=None, T=2, k=2, x=4096, xt=30, flags=0, out=4096, scale=None, ws=4096
 
 @pytest.mark.parametrize("kw,st,msg", [
     (dict(L=_layer(E=0)), 1, "n_experts = 0"), (dict(L=_layer(H=192)), 1, "hidden = 192"), (dict(L=_layer(I=64)), 1, "inter = 64"),
-    (dict(L=_layer(H=16512)), 2, "16512"), (dict(T=0), 1, "T = 0"), (dict(k=9), 1, "k = 9"),
+    (dict(L=_layer(H=16512)), 2, "16512"), (dict(T=0), 1, "T = 0"), (dict(k=9), 1, "k = 9"), (dict(T=1 << 24), 1, "hidden = 4294967296"),
     (dict(L=_layer(up=_mat(128, 512))), 1, "up is 128 x 512"), (dict(L=_layer(down=_mat(256, 128, expert_stride=256 * 127))), 1, "down.expert_stride"),
     (dict(L=_layer(shared=True, sh_down=qm.moe_fp8_matrix())), 1, "sh_down"), (dict(x=0), 1, "x or out is NULL"),
     (dict(out=0), 1, "x or out is NULL"), (dict(xt=12), 2, "x_type = 12"), (dict(flags=1), 1, "ffn_flags = 0x1"),
