@@ -147,12 +147,13 @@ __device__ __attribute__((aligned(16))) const uint32_t g_fp8_zero[4] = {0, 0, 0,
 // The compiler does not count these loads (with its own builtin it waits for
 // all of them before any LDS read, which leaves no stage in flight); the
 // kernels wait on vmcnt themselves.  No output register is written, and the
-// kernels hold nothing in m0.
+// kernels hold nothing in m0.  Volatile but no memory clobber: LDS reads of
+// other buffers may move past a copy, none moves past the waits and barriers.
 __device__ __forceinline__ void copy16_lds(const void* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src));
 }
 __device__ __forceinline__ void copy4_lds(const void* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src));
 }
 __device__ __forceinline__ uint64_t wave_uniform(uint64_t v) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
@@ -160,10 +161,10 @@ __device__ __forceinline__ uint64_t wave_uniform(uint64_t v) {
 }
 // The same from a wave-uniform base and a 32-bit offset per lane.
 __device__ __forceinline__ void copy16_lds(uint64_t base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base));
 }
 __device__ __forceinline__ void copy4_lds(uint64_t base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base));
 }
 template <int N>
 __device__ __forceinline__ void wait_vm() {

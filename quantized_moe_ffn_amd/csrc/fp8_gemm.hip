@@ -223,6 +223,17 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
     const uint32_t os = !PP && wave >= C::kSegs ? 0u : src_row(seg * 64 + lane) * (uint32_t)KB * 4;
 
     const uint32_t lds0 = lds_address(lds);
+    // copy c of block kb from a whole block (the ping-pong tiles issue them one by one between their MFMAs)
+    auto copy = [&](int kb, int c) {
+        const uint32_t la = lds0 + (kb % STAGES) * C::kStage + wave * 1024;
+        const uint64_t o = (uint64_t)kb * kFp8Block;
+        if (c < C::NA)
+            copy16_lds(ba[c < C::NA ? c : 0] + o, oa[c < C::NA ? c : 0], la + c * C::kWaves * 1024);
+        else
+            copy16_lds(bb + o, ob[c < C::NA ? 0 : c - C::NA], la + C::NR * 128 + (c - C::NA) * C::kWaves * 1024);
+        if (c == C::kLoads - 1 && (kb & 3) == 0)
+            copy16_lds(bs + 4 * (uint64_t)kb, os, lds0 + C::kRing + ((kb >> 2) & 1) * C::MT * 16 + seg * 1024);
+    };
     auto issue = [&](int kb) {
         const uint32_t st = lds0 + (kb % STAGES) * C::kStage;
         const uint32_t la = st + wave * 1024, lb = la + C::NR * 128;
@@ -327,8 +338,8 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
         // reads its fragments from LDS, the other runs MFMAs on those it holds.  A
         // half step ends at a barrier; group 1 runs one half step behind.  Stage s is
         // last read one half step before group 0 starts on stage s + 1, so its buffer
-        // takes stage s + STAGES from there on: group 0 issues it as it starts to read
-        // stage s + 1, group 1 as it computes its last part of stage s.
+        // takes stage s + STAGES from there on: group 0 copies into it during its first
+        // MFMAs of stage s + 1, group 1 during its last ones of stage s.
         constexpr int TB = EXACT ? 2 : 4, PH = WM / TB;
         static_assert(WM % TB == 0 && NWM == 2 && (C::NR + C::MT) % kWave == 0, "ping-pong shape");
         const int grp = wm;
@@ -365,7 +376,6 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
             block_scales(kb, wb0, wb1);
 #pragma unroll
             for (int ph = 0; ph < PH; ++ph) {
-                if (ph == 0 && grp == 0 && kb + STAGES - 1 < KB) issue(kb + STAGES - 1);
                 Fp8Frag<EXACT> fb[TB];
                 float s0[TB], s1[TB];
                 if (ph == 0) load_a(fa, st);
@@ -380,7 +390,9 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
                 for (int j = 0; j < TB; ++j) asm volatile("" : "+v"(s0[j]), "+v"(s1[j]));   // in this half step
                 if (ph == PH - 1 && grp == 1) landed(kb + 1);
                 meet();
-                if (ph == PH - 1 && grp == 1 && kb + STAGES < KB) issue(kb + STAGES);
+                // the stage this half step copies
+                const int cs = ph == 0 && grp == 0 ? kb + STAGES - 1 : (ph == PH - 1 && grp == 1 ? kb + STAGES : KB);
+                const bool more = cs < KB;
                 __builtin_amdgcn_s_setprio(1);
                 // tile q's MFMA goes out two tiles before its product is added, so the adds never wait on it
                 constexpr int Q = TB * WN;
@@ -395,6 +407,8 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
                 for (int q = 0; q < Q; ++q) {
                     t[q] = fa[q % WN].times(fb[q / WN]);
                     if (q >= 2) add(q - 2);
+                    if (q % (Q / C::kLoads) == Q / C::kLoads - 1 && q / (Q / C::kLoads) < C::kLoads && more)
+                        copy(cs, q / (Q / C::kLoads));
                 }
                 add(Q - 2);
                 add(Q - 1);
@@ -487,6 +501,16 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
     }
 }
 
+}  // namespace
+
+}  // namespace moe
+
+#include "fp8_stream.hip"
+
+namespace moe {
+
+namespace {
+
 // The work list of the grouped products from the bucket counts.
 __global__ void __launch_bounds__(1024) fp8_tiles_kernel(const int32_t* count, int npairs, int E, TileList tl) {
     __shared__ int s_wave[kWave + 1];
@@ -514,12 +538,17 @@ int fp8_max_tiles(int T, int k, int E, int has_shared, int mt) {
     return (int)(P / mt + act + (has_shared ? (T + mt - 1) / mt : 0));
 }
 
+// Persistent workgroups where the shape allows; else the tiles, with fp32 sums.
 template <int MODE, bool EXACT>
 hipError_t launch_grouped(const Fp8TileArgs& a, int64_t n_work, hipStream_t s) {
-    if (a.tl.mt == 32) return launch_tile<MODE, EXACT, false, 4, 1, 4, 2, 2>(a, n_work, s);
-    if (a.tl.mt == 64) return launch_tile<MODE, EXACT, false, 4, 2, 4, 2, 3>(a, n_work, s);
-    if (a.K % (4 * kFp8Block)) return launch_tile<MODE, EXACT, false, 4, 2, 4, 4, 3>(a, n_work, s);
-    return launch_tile<MODE, EXACT, true, 4, 2, 4, 4, 3>(a, n_work, s);
+    if (fp8_stream_k(a.K)) {
+        if (a.tl.mt == 32) return launch_stream<MODE, EXACT, 4, 1, 4, 2, 2>(a, n_work, s);
+        if (a.tl.mt == 64) return launch_stream<MODE, EXACT, 4, 2, 4, 2, 3>(a, n_work, s);
+        return launch_stream<MODE, EXACT, 4, 2, 4, 4, 3>(a, n_work, s);
+    }
+    if (a.tl.mt == 32) return launch_tile<MODE, true, false, 4, 1, 4, 2, 2>(a, n_work, s);
+    if (a.tl.mt == 64) return launch_tile<MODE, true, false, 4, 2, 4, 2, 3>(a, n_work, s);
+    return launch_tile<MODE, true, false, 4, 2, 4, 4, 3>(a, n_work, s);
 }
 
 template <bool EXACT>

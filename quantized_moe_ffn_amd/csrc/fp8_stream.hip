@@ -1,0 +1,341 @@
+// fp8_stream.hip — the grouped products of the expert layer as persistent
+// workgroups: one pipeline of copies and MFMAs runs through all the tiles of a
+// workgroup.
+//
+// The tiles of fp8_gemm.hip start cold: the list entry, the bucket, the pair ids
+// and the first copies are a chain of memory latencies, about 7 us against the
+// 4 to 16 us a tile's blocks take (down: 11.5 us a tile for four blocks; gate/up
+// of 4,096 tokens 212 us where the weights' 537 MB need about 100).  Here a
+// workgroup takes items j, j + step, ... of its XCD's contiguous part of the
+// list (item: 256 weight rows x one token tile; the row blocks of a tile are
+// neighbours, so workgroups that run at once share tokens and weights in L2),
+// and the copies run STAGES - 1 blocks ahead across item borders.  An item's
+// list entry, pair ids and weight scales are fetched one item ahead: the entry
+// by scalar loads, the rest by copies to LDS, so that the main loop holds no
+// load the compiler would wait for (its wait would drain the copies too).
+//
+// Needs K a multiple of 512 (token scales are copied four blocks at a time) and
+// at most 8,192 (the 64 weight scales of an item are one copy).
+#include "fp8.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kStreamMaxK = 64 * kFp8Block;
+inline bool fp8_stream_k(int K) { return K % (4 * kFp8Block) == 0 && K <= kStreamMaxK; }
+
+// Two words by scalar loads, waited for here.
+__device__ __forceinline__ void scalar_load2(const int32_t* p, const int32_t* q, int& a, int& b) {
+    asm volatile("s_load_dword %0, %2, 0x0\n\ts_load_dword %1, %3, 0x0\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&s"(a), "=&s"(b)
+                 : "s"(wave_uniform((uint64_t)p)), "s"(wave_uniform((uint64_t)q))
+                 : "memory");
+}
+
+// One work item, the same in every lane.  n_tok = 0: its bucket is not one a
+// routing pass leaves (the copies then read row 0 and nothing is stored).
+struct StreamItem {
+    int e, nb, mt0, n_tok, off;
+    bool shared;
+};
+
+template <int NWN, int NWM, int WN, int WM, int STAGES>
+struct StreamShape {
+    static constexpr int kWaves = NWN * NWM, kThreads = kWaves * kWave;
+    static constexpr int NR = NWN * WN * 16, MT = NWM * WM * 16;
+    static constexpr int NA = NR / 8 / kWaves, NB = MT / 8 / kWaves;
+    static constexpr int kLoads = NA + NB;            // copies of a wave in every stage
+    static constexpr int kSegs = MT < 64 ? 1 : MT / 64;
+    static constexpr int kTok = kSegs * 64;
+    static constexpr int kStage = (NR + MT) * 128, kRing = STAGES * kStage;
+    static constexpr int kXs = kTok * 16;             // token scales: [token][4 blocks], two buffers
+    static constexpr int kMeta = kTok * 4 + 512;      // an item's pair ids and 2 x 64 weight scales, three buffers
+    static constexpr int kLds = kRing + 2 * kXs + 3 * kMeta;
+    static_assert(NA * 8 * kWaves == NR && NB * 8 * kWaves == MT && NR == 256, "copies divide evenly");
+    static_assert(kWaves >= kSegs + 2 && kLds + NWN * MT * 4 <= 160 * 1024 && STAGES <= 4, "shape");
+};
+
+template <int MODE, bool EXACT, int NWN, int NWM, int WN, int WM, int STAGES>
+__global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8TileArgs a) {
+    using C = StreamShape<NWN, NWM, WN, WM, STAGES>;
+    constexpr bool kGu = MODE == kFp8GateUp;
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+    __shared__ uint32_t s_amax[kGu ? NWN : 1][C::MT];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wn = wave % NWN, wm = wave / NWN;
+    const int g = lane >> 4, r16 = lane & 15;
+    const int K = a.K, KB = K / kFp8Block, P = a.T * a.k;
+    const uint32_t lds0 = lds_address(lds);
+
+    int n_tiles, unused;
+    scalar_load2(a.tl.n_tiles, a.tl.n_tiles, n_tiles, unused);
+    const int n_work = n_tiles * a.nblocks;
+    const int chunk = (n_work + 7) / 8, step = gridDim.x / 8;
+    const int first = (blockIdx.x % 8) * chunk + blockIdx.x / 8;
+    const int lim = min((int)(blockIdx.x % 8 + 1) * chunk, n_work);
+    if (first >= lim) return;
+    const int total = ((lim - first - 1) / step + 1) * KB;   // stages of this workgroup
+
+    auto load_item = [&](int w) {
+        StreamItem it;
+        const int u = w / a.nblocks;
+        it.nb = w - u * a.nblocks;
+        scalar_load2(a.tl.tile_e + u, a.tl.tile_m0 + u, it.e, it.mt0);
+        it.shared = it.e >= a.E;
+        int c = a.T;
+        it.off = P;   // the shared expert's rows of h follow the pairs'
+        if (!it.shared) {
+            scalar_load2(a.count + it.e, a.offset + it.e, c, it.off);
+            if (c < 0 || it.off < 0 || (int64_t)it.off + c > P) {   // buffers not from a routing pass
+                if (tid == 0) raise_error(kErrPairRange);
+                c = it.off = it.mt0 = 0;
+            }
+        }
+        it.n_tok = max(0, min(C::MT, c - it.mt0));
+        return it;
+    };
+    // Copies of an item's pair ids and weight scales into buffer b.
+    auto fetch_meta = [&](const StreamItem& it, int b) {
+        const uint32_t at = lds0 + C::kRing + 2 * C::kXs + b * C::kMeta;
+        if (wave < C::kSegs) {
+            const int m = min(wave * 64 + lane, max(it.n_tok, 1) - 1);
+            if (!it.shared)
+                copy4_lds(wave_uniform((uint64_t)(a.pair + it.off + it.mt0)), (uint32_t)m * 4, at + wave * 256);
+        } else if (wave < C::kSegs + 2) {
+            const int q = wave - C::kSegs;
+            const int sb = kGu ? it.nb : min(2 * it.nb + q, (a.N - 1) / kFp8Block);
+            const float* sc = kGu && q ? (it.shared ? a.s1.scale : a.w1.scale) : (it.shared ? a.s0.scale : a.w0.scale);
+            const int64_t rb = it.shared ? 0 : (int64_t)it.e * ((a.N + kFp8Block - 1) / kFp8Block);
+            copy4_lds(wave_uniform((uint64_t)(sc + (rb + sb) * KB)), (uint32_t)min(lane, KB - 1) * 4,
+                      at + C::kTok * 4 + q * 256);
+        }
+    };
+
+    // The item whose blocks are being copied: 32-bit offsets from wave-uniform bases.
+    const int lr = lane >> 3, ca = ((lane & 7) ^ lr) * 16;
+    uint64_t ba[C::NA], bb = 0, bs = 0;
+    uint32_t oa[C::NA], ob[C::NB], os = 0;
+    auto setup = [&](const StreamItem& it, int b) {
+        const int* pr = reinterpret_cast<const int*>(lds + C::kRing + 2 * C::kXs + b * C::kMeta);
+        const uint8_t* d0 = it.shared ? a.s0.data : a.w0.data + (int64_t)it.e * a.w0.expert_stride;
+        const uint8_t* d1 = !kGu ? d0 : (it.shared ? a.s1.data : a.w1.data + (int64_t)it.e * a.w1.expert_stride);
+        const int r0 = (int)(it.shared ? a.s0.row_stride : a.w0.row_stride);
+        const int r1 = !kGu ? r0 : (int)(it.shared ? a.s1.row_stride : a.w1.row_stride);
+#pragma unroll
+        for (int i = 0; i < C::NA; ++i) {
+            const int R8 = (wave + i * C::kWaves) * 8;
+            if constexpr (kGu) {
+                const int w_ = R8 / (WN * 16), t_ = (R8 / 16) % WN, r_ = R8 & 15;
+                const int row = it.nb * (C::NR / 2) + w_ * (WN / 2 * 16) + (t_ % (WN / 2)) * 16 + r_;
+                const bool up = t_ >= WN / 2;
+                ba[i] = wave_uniform((uint64_t)(up ? d1 : d0) + (uint64_t)row * (uint32_t)(up ? r1 : r0));
+                oa[i] = (uint32_t)(lr * (up ? r1 : r0) + ca);
+            } else {
+                const int row0 = it.nb * C::NR;
+                ba[i] = wave_uniform((uint64_t)d0 + (uint64_t)row0 * (uint32_t)r0);
+                oa[i] = (uint32_t)((min(row0 + R8 + lr, a.N - 1) - row0) * r0 + ca);
+            }
+        }
+        // token operand: gate/up gathers rows of x, down reads the bucket's rows of h
+        const int last = max(it.n_tok, 1) - 1;
+        auto src = [&](int m) -> uint32_t {
+            m = min(m, last);
+            if constexpr (!kGu) return m;
+            if (it.shared) return it.mt0 + m;
+            const uint32_t p = pr[m];
+            if (p >= (uint32_t)P) raise_error(kErrPairRange);
+            return p < (uint32_t)P ? p / (uint32_t)a.k : 0u;
+        };
+        const int64_t tok0 = kGu ? 0 : (int64_t)it.off + it.mt0;
+        bb = wave_uniform((uint64_t)(a.xq + tok0 * K));
+        bs = wave_uniform((uint64_t)(a.xs + tok0 * KB));
+#pragma unroll
+        for (int i = 0; i < C::NB; ++i) ob[i] = src((wave + i * C::kWaves) * 8 + lr) * (uint32_t)K + ca;
+        os = src(wave % C::kSegs * 64 + lane) * (uint32_t)KB * 4;
+    };
+
+    StreamItem cur = load_item(first), nxt = cur;
+    int iw = first, ikb = 0, islot = 0, ixs = 0, ibuf = 0;   // item, block, ring slot, scale and meta buffer of the copies
+    fetch_meta(cur, 0);
+    wait_vm<0>();
+    lds_barrier();
+    setup(cur, 0);
+    if (first + step < lim) {
+        nxt = load_item(first + step);
+        fetch_meta(nxt, 1);
+    }
+    // Copy c of the next block (kLoads of them, then possibly the token scales).  They go out between the
+    // MFMAs: the address unit takes about 16 cycles for each, 768 a block, which would otherwise stand
+    // between the barrier and the first LDS reads.
+    auto copy = [&](int c) {
+        const uint32_t la = lds0 + islot * C::kStage + wave * 1024;
+        const uint64_t o = (uint64_t)ikb * kFp8Block;
+        if (c < C::NA)
+            copy16_lds(ba[c < C::NA ? c : 0] + o, oa[c < C::NA ? c : 0], la + c * C::kWaves * 1024);
+        else
+            copy16_lds(bb + o, ob[c < C::NA ? 0 : c - C::NA], la + C::NR * 128 + (c - C::NA) * C::kWaves * 1024);
+    };
+    // After the copies: moves on to the next block; past an item's last one to the next item, whose pair ids
+    // were copied a whole item ago (K/128 >= STAGES blocks: older than the block just waited for).
+    auto advance = [&]() {
+        if ((ikb & 3) == 0) {
+            copy16_lds(wave_uniform(bs + 4 * (uint64_t)ikb), os, lds0 + C::kRing + ixs * C::kXs + wave % C::kSegs * 1024);
+            ixs ^= 1;
+        }
+        islot = islot + 1 == STAGES ? 0 : islot + 1;
+        if (++ikb == KB) {
+            ikb = 0;
+            iw += step;
+            if (iw < lim) {
+                ibuf = ibuf == 2 ? 0 : ibuf + 1;
+                cur = nxt;
+                setup(cur, ibuf);
+                if (iw + step < lim) {
+                    nxt = load_item(iw + step);
+                    fetch_meta(nxt, ibuf == 2 ? 0 : ibuf + 1);
+                }
+            }
+        }
+    };
+
+    // the item being computed
+    StreamItem ci = cur;
+    int cbuf = 0, kb = 0, st = 0, xs = 0;
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {   // an item has at least STAGES blocks
+#pragma unroll
+        for (int c = 0; c < C::kLoads; ++c) copy(c);
+        advance();
+    }
+
+    const int c0 = (g ^ (r16 & 7)) * 16, c1 = c0 ^ 64;
+    const unsigned char* la0 = lds + (wn * WN * 16 + r16) * 128 + c0;
+    const unsigned char* la1 = lds + (wn * WN * 16 + r16) * 128 + c1;
+    const unsigned char* lb0 = lds + C::NR * 128 + (wm * WM * 16 + r16) * 128 + c0;
+    const unsigned char* lb1 = lds + C::NR * 128 + (wm * WM * 16 + r16) * 128 + c1;
+    const unsigned char* lsx = lds + C::kRing + (wm * WM * 16 + r16) * 16;
+    v4f_f8 acc[WN][WM] = {};
+    for (int s = 0; s < total; ++s) {
+        if (s + STAGES - 2 < total)
+            wait_vm<(STAGES - 2) * C::kLoads>();
+        else
+            wait_vm<0>();
+        lds_barrier();
+        const bool more = s + STAGES - 1 < total;
+        const float* pw = reinterpret_cast<const float*>(lds + C::kRing + 2 * C::kXs + cbuf * C::kMeta + C::kTok * 4);
+        // down: 256 rows are two scale blocks, four waves of 64 rows
+        const float wb0 = pw[(kGu ? 0 : (wn >> 1) * 64) + kb], wb1 = kGu ? pw[64 + kb] : 0.f;
+        Fp8Frag<EXACT> fa[WN];
+#pragma unroll
+        for (int i = 0; i < WN; ++i)
+            fa[i].set(*reinterpret_cast<const int4*>(la0 + st + i * 2048), *reinterpret_cast<const int4*>(la1 + st + i * 2048));
+#pragma unroll
+        for (int j = 0; j < WM; ++j) {
+            Fp8Frag<EXACT> fb;
+            fb.set(*reinterpret_cast<const int4*>(lb0 + st + j * 2048), *reinterpret_cast<const int4*>(lb1 + st + j * 2048));
+            const float x = *reinterpret_cast<const float*>(lsx + xs + j * 256 + (kb & 3) * 4);
+            const float s0 = x * wb0, s1 = kGu ? x * wb1 : 0.f;
+#pragma unroll
+            for (int i = 0; i < WN; ++i) {
+                const v4f_f8 t = fa[i].times(fb);
+                const float sc = kGu && i >= WN / 2 ? s1 : s0;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(t[v], sc, acc[i][j][v]);
+            }
+            if (more) {
+#pragma unroll
+                for (int c = C::kLoads * j / WM; c < C::kLoads * (j + 1) / WM; ++c) copy(c);
+            }
+        }
+        if (more) advance();
+        st = st + C::kStage == C::kRing ? 0 : st + C::kStage;
+        if ((kb & 3) == 3) xs ^= C::kXs;
+        if (++kb < KB) continue;
+
+        // The item's results: value v of acc[i][j] is weight row 16*i + 4*g + v, token 16*j + r16 of the wave.
+        // The copies of the next item's first blocks are in flight.
+        if constexpr (kGu) {
+            constexpr int HI = WN / 2;
+#pragma unroll
+            for (int j = 0; j < WM; ++j) {
+                uint32_t mx = 0;
+#pragma unroll
+                for (int i = 0; i < HI; ++i)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const float h = silu_f32(acc[i][j][v]) * acc[i + HI][j][v];
+                        acc[i][j][v] = h;
+                        mx = max(mx, __float_as_uint(h) & 0x7FFFFFFFu);
+                    }
+                mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, kWave));
+                mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, kWave));
+                if (g == 0) s_amax[wn][(wm * WM + j) * 16 + r16] = mx;
+            }
+            lds_barrier();
+            const int64_t row0 = (int64_t)ci.off + ci.mt0;
+#pragma unroll
+            for (int j = 0; j < WM; ++j) {
+                const int m = (wm * WM + j) * 16 + r16;
+                uint32_t mx = s_amax[0][m];
+#pragma unroll
+                for (int q = 1; q < NWN; ++q) mx = max(mx, s_amax[q][m]);
+                const bool fin = mx < 0x7F800000u;
+                if (m >= ci.n_tok) continue;
+                if (!fin) raise_error(kErrActNonFinite);
+                const Fp8Rule rule(__uint_as_float(fin ? mx : 0u));
+#pragma unroll
+                for (int i = 0; i < HI; ++i) {
+                    const uint32_t q = fin ? rule.pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]) : 0u;
+                    const int col = ci.nb * (C::NR / 2) + (wn * HI + i) * 16 + 4 * g;
+                    *reinterpret_cast<uint32_t*>(a.hq + (row0 + m) * a.N + col) = q;
+                }
+                if (wn == 0 && g == 0) a.hs[(row0 + m) * (a.N / kFp8Block) + ci.nb] = rule.d;
+            }
+        } else {
+            const int* pr = reinterpret_cast<const int*>(lds + C::kRing + 2 * C::kXs + cbuf * C::kMeta);
+            const ElemType pt = a.pair_bf16 ? ElemType::kBF16 : ElemType::kF32;
+            void* base = ci.shared ? a.y_shared : a.y_pair;
+#pragma unroll
+            for (int j = 0; j < WM; ++j) {
+                const int m = (wm * WM + j) * 16 + r16;
+                const int row = ci.shared ? ci.mt0 + m : pr[m];
+                if (m >= ci.n_tok) continue;
+                if (!ci.shared && (uint32_t)row >= (uint32_t)P) {
+                    raise_error(kErrPairRange);
+                    continue;
+                }
+#pragma unroll
+                for (int i = 0; i < WN; ++i) {
+                    const int n = ci.nb * C::NR + (wn * WN + i) * 16 + 4 * g;
+                    const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                    if (n < a.N) store4(base, (int64_t)row * a.N + n, pt, v, a.N - n, true);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < WN; ++i)
+#pragma unroll
+            for (int j = 0; j < WM; ++j) acc[i][j] = v4f_f8{0.f, 0.f, 0.f, 0.f};
+        kb = 0;
+        ci = cur;   // the copies are STAGES - 1 blocks ahead: in the next item
+        cbuf = cbuf == 2 ? 0 : cbuf + 1;
+    }
+}
+
+constexpr int kCus = 256;
+
+template <int MODE, bool EXACT, int NWN, int NWM, int WN, int WM, int STAGES>
+hipError_t launch_stream(const Fp8TileArgs& a, int64_t n_work, hipStream_t s) {
+    using C = StreamShape<NWN, NWM, WN, WM, STAGES>;
+    const int64_t per_cu = (C::kLds + NWN * C::MT * 4) * 2 <= 160 * 1024 ? 2 : 1;
+    const int64_t want = (n_work + 7) / 8 * 8;
+    const unsigned grid = (unsigned)(want < per_cu * kCus ? want : per_cu * kCus);
+    fp8_stream_kernel<MODE, EXACT, NWN, NWM, WN, WM, STAGES><<<grid, C::kThreads, C::kLds, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace moe
