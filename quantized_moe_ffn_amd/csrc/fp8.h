@@ -23,8 +23,6 @@ struct ScoreRule {
     const float* bias;  // [E] or null
 };
 
-// The grouped products' work list: tile i of expert e covers rows mt*i .. of
-// its bucket (TileList, kernels.h), written by the routing launch when mt > 0.
 hipError_t launch_route_scored(const float* logits, int T, int E, int k, const ScoreRule& rule, const RoutingPtrs& r,
                                void* ws, hipStream_t s);
 
@@ -45,6 +43,12 @@ struct Fp8Mat {
 
 hipError_t launch_quantize_fp8(const void* x, ElemType xt, int64_t ldx, int T, int H, uint8_t* xq, float* xs,
                                hipStream_t s);
+
+// A layer call's routing: launch_route_scored, x [T][H] quantised by extra workgroups of the same launch and, with
+// tl.mt > 0, the grouped products' work list (TileList, kernels.h).
+hipError_t launch_route_quantize_fp8(const float* logits, int T, int E, int k, const ScoreRule& rule,
+                                     const RoutingPtrs& r, void* ws, const TileList& tl, const void* x, ElemType xt, int H,
+                                     uint8_t* xq, float* xs, hipStream_t s);
 
 struct Fp8MatmulArgs {
     const uint8_t* xq;
@@ -73,7 +77,8 @@ struct Fp8FfnArgs {
     float* hf;               // workspace of the few-pair kernels: h in fp32, [T*k (+T)][I]
 };
 size_t fp8_tiles_bytes(int T, int k, int E, int has_shared);
-hipError_t launch_ffn_fp8(const Fp8FfnArgs& a, hipStream_t s);
+TileList fp8_tile_list(const Fp8FfnArgs& f);   // the list launch_ffn_fp8 works through, in f.tiles
+hipError_t launch_ffn_fp8(const Fp8FfnArgs& a, bool tiles_ready, hipStream_t s);
 
 // Few pairs: T*k up to this, and up to the expert count, so that few pairs share an expert's read.
 constexpr int kFewPairs = 64;

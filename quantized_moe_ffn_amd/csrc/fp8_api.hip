@@ -262,7 +262,7 @@ moe_status moe_expert_ffn_fp8(const moe_fp8_layer* L, const moe_routing* r, int3
     if (moe::fp8_few_pairs(T, k, L->n_experts))
         return finish(from_hip(moe::launch_skinny_ffn(a, moe::Fp8CombineArgs{}, stream), "moe_expert_ffn_fp8 launch"),
                       stream, "moe_expert_ffn_fp8");
-    return finish(from_hip(moe::launch_ffn_fp8(a, stream), "moe_expert_ffn_fp8 launch"), stream, "moe_expert_ffn_fp8");
+    return finish(from_hip(moe::launch_ffn_fp8(a, false, stream), "moe_expert_ffn_fp8 launch"), stream, "moe_expert_ffn_fp8");
 }
 
 size_t moe_forward_fp8_workspace_bytes(const moe_fp8_layer* L, int32_t T, int32_t k, uint32_t ffn_flags) {
@@ -301,15 +301,16 @@ moe_status moe_forward_fp8(const moe_fp8_layer* L, const moe_route_spec* spec, c
     a.y_shared = L->has_shared ? ws + wl.ysh : nullptr;
     a.pair_bf16 = bf16 ? 1 : 0;
     a.exact = xt == moe::ElemType::kBF16 ? 0 : 1;
-    hipError_t e = moe::launch_route_scored(logits, T, L->n_experts, k, to_rule(*spec), a.r, ws + wl.route, stream);
-    if (e != hipSuccess) return from_hip(e, "moe_forward_fp8: routing launch");
-    e = moe::launch_quantize_fp8(x, xt, L->hidden, T, L->hidden, (uint8_t*)(ws + wl.xq), (float*)(ws + wl.xs), stream);
-    if (e != hipSuccess) return from_hip(e, "moe_forward_fp8: quantisation launch");
+    const bool few = moe::fp8_few_pairs(T, k, L->n_experts);
+    const moe::TileList tl = few ? moe::TileList{} : moe::fp8_tile_list(a);
+    hipError_t e = moe::launch_route_quantize_fp8(logits, T, L->n_experts, k, to_rule(*spec), a.r, ws + wl.route, tl, x, xt,
+                                                  L->hidden, (uint8_t*)(ws + wl.xq), (float*)(ws + wl.xs), stream);
+    if (e != hipSuccess) return from_hip(e, "moe_forward_fp8: routing and quantisation launch");
     const moe::Fp8CombineArgs c{a.y_pair, a.y_shared, a.pair_bf16, r->w, shared_scale, out, xt, T, k, L->hidden};
-    if (moe::fp8_few_pairs(T, k, L->n_experts))
+    if (few)
         return finish(from_hip(moe::launch_skinny_ffn(a, c, stream), "moe_forward_fp8: expert FFN launch"), stream,
                       "moe_forward_fp8");
-    e = moe::launch_ffn_fp8(a, stream);
+    e = moe::launch_ffn_fp8(a, true, stream);
     if (e != hipSuccess) return from_hip(e, "moe_forward_fp8: expert FFN launch");
     return finish(from_hip(moe::launch_combine_fp8(c, stream), "moe_forward_fp8: combine launch"), stream,
                   "moe_forward_fp8");

@@ -565,18 +565,22 @@ size_t fp8_tiles_bytes(int T, int k, int E, int has_shared) {
     return (size_t)(2 * (int64_t)fp8_max_tiles(T, k, E, has_shared, fp8_tile_tokens(T, k, E)) + 1) * sizeof(int32_t);
 }
 
-hipError_t launch_ffn_fp8(const Fp8FfnArgs& f, hipStream_t s) {
-    const int mt = fp8_tile_tokens(f.T, f.k, f.E);
-    const int max_t = fp8_max_tiles(f.T, f.k, f.E, f.has_shared, mt);
+TileList fp8_tile_list(const Fp8FfnArgs& f) {
     TileList tl{};
+    tl.mt = fp8_tile_tokens(f.T, f.k, f.E);
+    tl.max_t = fp8_max_tiles(f.T, f.k, f.E, f.has_shared, tl.mt);
     tl.tile_e = f.tiles;
-    tl.tile_m0 = f.tiles + max_t;
-    tl.n_tiles = f.tiles + 2 * (int64_t)max_t;
-    tl.mt = mt;
-    tl.max_t = max_t;
+    tl.tile_m0 = f.tiles + tl.max_t;
+    tl.n_tiles = f.tiles + 2 * (int64_t)tl.max_t;
     tl.T = f.T;
     tl.has_shared = f.has_shared;
-    fp8_tiles_kernel<<<1, 1024, 0, s>>>(f.r.count, f.T * f.k, f.E, tl);
+    return tl;
+}
+
+hipError_t launch_ffn_fp8(const Fp8FfnArgs& f, bool tiles_ready, hipStream_t s) {
+    const TileList tl = fp8_tile_list(f);
+    const int max_t = tl.max_t;
+    if (!tiles_ready) fp8_tiles_kernel<<<1, 1024, 0, s>>>(f.r.count, f.T * f.k, f.E, tl);
     Fp8TileArgs a{};
     a.w0 = f.gate;
     a.w1 = f.up;

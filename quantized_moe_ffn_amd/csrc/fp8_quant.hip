@@ -78,34 +78,47 @@ __device__ __forceinline__ void quantize_fp8_lanes(int64_t grp, int64_t stride, 
     }
 }
 
+// The quantiser's work, in workgroups of 1,024 threads (alone, or carried by the routing launches of a layer call).
 template <typename XT>
-__global__ void __launch_bounds__(256) quantize_fp8_kernel(const XT* __restrict__ x, int64_t ldx, int64_t n_blocks,
-                                                           int nb, int H, uint8_t* __restrict__ xq,
-                                                           float* __restrict__ xs) {
-    constexpr int kGroups = 256 / 16;
-    quantize_fp8_lanes<XT>((int64_t)blockIdx.x * kGroups * kFp8QuantIters + threadIdx.x / 16, kGroups, x, ldx, n_blocks,
-                           nb, H, xq, xs);
+struct ActQuant {
+    static constexpr int kGroups = 1024 / 16;
+    const XT* x = nullptr;
+    int64_t ldx = 0, n_blocks = 0;
+    int nb = 1, H = 0;
+    uint8_t* xq = nullptr;
+    float* xs = nullptr;
+    ActQuant() = default;
+    ActQuant(const void* x_, int64_t ldx_, int T, int H_, uint8_t* xq_, float* xs_)
+        : x((const XT*)x_), ldx(ldx_), nb((H_ + kFp8Block - 1) / kFp8Block), H(H_), xq(xq_), xs(xs_) {
+        n_blocks = (int64_t)T * nb;
+    }
+    unsigned groups() const {
+        return (unsigned)((n_blocks + kGroups * kFp8QuantIters - 1) / (kGroups * kFp8QuantIters));
+    }
+    __device__ __forceinline__ void run(int wg) const {
+        quantize_fp8_lanes<XT>((int64_t)wg * kGroups * kFp8QuantIters + threadIdx.x / 16, kGroups, x, ldx, n_blocks, nb, H,
+                               xq, xs);
+    }
+};
+
+template <typename XT>
+__global__ void __launch_bounds__(1024) quantize_fp8_kernel(const ActQuant<XT> q) {
+    q.run(blockIdx.x);
 }
 
-inline unsigned quantize_fp8_grid(int T, int H) {
-    const int64_t n = (int64_t)T * ((H + kFp8Block - 1) / kFp8Block);
-    return (unsigned)((n + 16 * kFp8QuantIters - 1) / (16 * kFp8QuantIters));
+template <typename XT>
+hipError_t launch_quantize_fp8_t(const ActQuant<XT>& q, hipStream_t s) {
+    quantize_fp8_kernel<XT><<<q.groups(), 1024, 0, s>>>(q);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_quantize_fp8(const void* x, ElemType xt, int64_t ldx, int T, int H, uint8_t* xq, float* xs,
                                hipStream_t s) {
-    const int nb = (H + kFp8Block - 1) / kFp8Block;
-    const int64_t n = (int64_t)T * nb;
-    const unsigned grid = quantize_fp8_grid(T, H);
-    if (xt == ElemType::kF32)
-        quantize_fp8_kernel<float><<<grid, 256, 0, s>>>((const float*)x, ldx, n, nb, H, xq, xs);
-    else if (xt == ElemType::kF16)
-        quantize_fp8_kernel<_Float16><<<grid, 256, 0, s>>>((const _Float16*)x, ldx, n, nb, H, xq, xs);
-    else
-        quantize_fp8_kernel<__bf16><<<grid, 256, 0, s>>>((const __bf16*)x, ldx, n, nb, H, xq, xs);
-    return hipGetLastError();
+    if (xt == ElemType::kF32) return launch_quantize_fp8_t(ActQuant<float>(x, ldx, T, H, xq, xs), s);
+    if (xt == ElemType::kF16) return launch_quantize_fp8_t(ActQuant<_Float16>(x, ldx, T, H, xq, xs), s);
+    return launch_quantize_fp8_t(ActQuant<__bf16>(x, ldx, T, H, xq, xs), s);
 }
 
 }  // namespace moe

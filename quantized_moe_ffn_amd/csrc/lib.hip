@@ -3,8 +3,8 @@
 // its error word, routing buffers and argument checks.
 #include "libmoe.hip"
 
-#include "route_scored.hip"
 #include "fp8_quant.hip"
+#include "route_scored.hip"
 #include "fp8_skinny.hip"
 #include "fp8_gemm.hip"
 #include "fp8_api.hip"
