@@ -452,8 +452,10 @@ size_t moe_forward_fp8_workspace_bytes(const moe_fp8_layer* L, int32_t T, int32_
  * shared_scale[t], or 1 when NULL (non-NULL needs a shared expert).  x and out
  * [T][H] of x_type, contiguous and 16-byte aligned; out may be x.  The per-pair
  * and shared outputs stay in the workspace: as fp32, or with ffn_flags =
- * MOE_FFN_PAIR_BF16 as bf16 (out then moves by at most 2^-8 * (sum_j |w_j*y_j| +
- * |s_t*y_shared|) per element); ffn_flags is otherwise 0. */
+ * MOE_FFN_PAIR_BF16 in bf16's size, as fp16 values times one power of two for
+ * each 64 columns of a row (each y then moves by at most 2^-11 * |y| + 2^-25 of
+ * the largest of its 64 columns); ffn_flags is otherwise 0.  Batches of few
+ * pairs combine in the down projection's kernel, without a hand-off. */
 moe_status moe_forward_fp8(const moe_fp8_layer* L, const moe_route_spec* spec, const float* logits, const void* x,
                            int32_t x_type, int32_t T, int32_t k, uint32_t ffn_flags, const moe_routing* r,
                            const float* shared_scale, void* out, void* workspace, size_t ws_bytes,

@@ -69,9 +69,10 @@ struct Fp8FfnArgs {
     const float* xs;         // [T][H/128]
     uint8_t* hq;             // workspace [T*k (+T)][I], bucket order, then the shared expert's rows
     float* hs;               // workspace [T*k (+T)][I/128]
-    void* y_pair;            // [T*k][H] fp32 or bf16
-    void* y_shared;          // [T][H], the same type
-    int pair_bf16;
+    void* y_pair;            // [T*k][H] fp32, or fp16 with scales (pair16)
+    void* y_shared;          // [T][H], the same
+    float* y_scale;          // pair16: [T*k (+T)][H/64]
+    int pair16;
     int exact;               // products with fp32 sums throughout (fp8_gemm.hip)
     int32_t* tiles;          // workspace: the work list (fp8_tiles_bytes)
     float* hf;               // workspace of the few-pair kernels: h in fp32, [T*k (+T)][I]
@@ -86,9 +87,10 @@ constexpr int kMaxSlots = 17;   // top-k and the shared expert
 inline bool fp8_few_pairs(int T, int k, int E) { return T * k <= kFewPairs && T * k <= E; }
 
 struct Fp8CombineArgs {
-    const void* y_pair;      // fp32 or bf16 [T*k][H]
-    const void* y_shared;    // the same type [T][H], or null
-    int pair_bf16;
+    const void* y_pair;      // [T*k][H] fp32, or fp16 with scales (pair16)
+    const void* y_shared;    // [T][H], the same, or null
+    const float* y_scale;    // pair16: [T*k (+T)][H/64]
+    int pair16;
     const float* w;          // [T][k]
     const float* shared_scale;
     void* out;
@@ -99,6 +101,13 @@ struct Fp8CombineArgs {
 hipError_t launch_skinny_ffn(const Fp8FfnArgs& f, const Fp8CombineArgs& c, hipStream_t s);
 hipError_t launch_skinny_matmul(const Fp8MatmulArgs& a, hipStream_t s);
 hipError_t launch_combine_fp8(const Fp8CombineArgs& a, hipStream_t s);
+
+// The 16-bit hand-off of the per-pair outputs: each 64 columns of a row are fp16
+// values times one power of two, the exponent of the largest.  Same bytes as
+// bf16 (and 1/16 of a byte a value for the scales), an eighth of its rounding,
+// and no overflow: with bf16 the rounding of the pairs was as large as that of a
+// bf16 output, and its error against 64 bits 1.65 times the plain form's.
+constexpr int kPairBlock = 64;
 
 // ------------------------------------------------------------------ device helpers
 

@@ -127,10 +127,10 @@ Fp8FfnWorkspace fp8_ffn_layout(const moe_fp8_layer* L, int T, int k) {
 }
 
 struct Fp8ForwardWorkspace {
-    size_t route, route_bytes, ffn, xq, xs, yp, ysh, total;
+    size_t route, route_bytes, ffn, xq, xs, yp, ysh, ysc, total;
 };
 
-Fp8ForwardWorkspace fp8_forward_layout(const moe_fp8_layer* L, int T, int k, bool bf16) {
+Fp8ForwardWorkspace fp8_forward_layout(const moe_fp8_layer* L, int T, int k, bool pair16) {
     Fp8ForwardWorkspace w{};
     size_t off = 0;
     w.route = off;
@@ -147,9 +147,12 @@ Fp8ForwardWorkspace fp8_forward_layout(const moe_fp8_layer* L, int T, int k, boo
         return w;
     }
     w.yp = off;
-    off += align_up((size_t)T * k * L->hidden * (bf16 ? 2 : 4), 256);
+    off += align_up((size_t)T * k * L->hidden * (pair16 ? 2 : 4), 256);
     w.ysh = off;
-    if (L->has_shared) off += align_up((size_t)T * L->hidden * (bf16 ? 2 : 4), 256);
+    if (L->has_shared) off += align_up((size_t)T * L->hidden * (pair16 ? 2 : 4), 256);
+    w.ysc = off;
+    if (pair16)
+        off += align_up(((size_t)T * k + (L->has_shared ? T : 0)) * (L->hidden / moe::kPairBlock) * sizeof(float), 256);
     w.total = off;
     return w;
 }
@@ -288,8 +291,8 @@ moe_status moe_forward_fp8(const moe_fp8_layer* L, const moe_route_spec* spec, c
         return fail(MOE_ERR_INVALID_ARGUMENT, "shared_scale given for a layer without a shared expert");
     if (!aligned(x, 16) || !aligned(out, 16) || (shared_scale && !aligned(shared_scale, 4)))
         return fail(MOE_ERR_INVALID_ARGUMENT, "x and out must be 16-byte aligned, shared_scale 4-byte aligned");
-    const bool bf16 = ffn_flags != 0;
-    const Fp8ForwardWorkspace wl = fp8_forward_layout(L, T, k, bf16);
+    const bool pair16 = ffn_flags != 0;
+    const Fp8ForwardWorkspace wl = fp8_forward_layout(L, T, k, pair16);
     if (!workspace || ws_bytes < wl.total)
         return fail(MOE_ERR_WORKSPACE, "fp8 forward workspace: %zu bytes given, %zu needed", ws_bytes, wl.total);
     if (!aligned(workspace, 256)) return fail(MOE_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
@@ -299,14 +302,15 @@ moe_status moe_forward_fp8(const moe_fp8_layer* L, const moe_route_spec* spec, c
     a.xs = (float*)(ws + wl.xs);
     a.y_pair = ws + wl.yp;
     a.y_shared = L->has_shared ? ws + wl.ysh : nullptr;
-    a.pair_bf16 = bf16 ? 1 : 0;
+    a.y_scale = (float*)(ws + wl.ysc);
+    a.pair16 = pair16 ? 1 : 0;
     a.exact = xt == moe::ElemType::kBF16 ? 0 : 1;
     const bool few = moe::fp8_few_pairs(T, k, L->n_experts);
     const moe::TileList tl = few ? moe::TileList{} : moe::fp8_tile_list(a);
     hipError_t e = moe::launch_route_quantize_fp8(logits, T, L->n_experts, k, to_rule(*spec), a.r, ws + wl.route, tl, x, xt,
                                                   L->hidden, (uint8_t*)(ws + wl.xq), (float*)(ws + wl.xs), stream);
     if (e != hipSuccess) return from_hip(e, "moe_forward_fp8: routing and quantisation launch");
-    const moe::Fp8CombineArgs c{a.y_pair, a.y_shared, a.pair_bf16, r->w, shared_scale, out, xt, T, k, L->hidden};
+    const moe::Fp8CombineArgs c{a.y_pair, a.y_shared, a.y_scale, a.pair16, r->w, shared_scale, out, xt, T, k, L->hidden};
     if (few)
         return finish(from_hip(moe::launch_skinny_ffn(a, c, stream), "moe_forward_fp8: expert FFN launch"), stream,
                       "moe_forward_fp8");

@@ -62,7 +62,8 @@ struct Fp8TileArgs {
     float* hs;
     void* y_pair;              // down: out
     void* y_shared;
-    int pair_bf16;
+    float* y_scale;
+    int pair16;
     int nblocks;               // row blocks
 };
 
@@ -91,6 +92,41 @@ __device__ __forceinline__ void store4(void* base, int64_t idx, ElemType t, cons
         for (int i = 0; i < 4; ++i)
             if (i < n_ok) p[i] = h[i];
     }
+}
+
+// A wave's 64 columns (from n0, one kPairBlock) of an output row: lane group g of the row's four lanes holds
+// columns 16*i + 4*g + v.  Every lane calls it; row < 0: not stored.
+template <int WN>
+__device__ __forceinline__ void store_row64(const v4f_f8 (&y)[WN], void* base, float* scale, int pair16, int64_t row, int n0,
+                                            int N) {
+    static_assert(WN * 16 == kPairBlock, "one block a wave");
+    const int g = (threadIdx.x & (kWave - 1)) >> 4;
+    if (!pair16) {
+        if (row < 0 || n0 >= N) return;
+        float* p = (float*)base + row * N + n0 + 4 * g;
+#pragma unroll
+        for (int i = 0; i < WN; ++i) *reinterpret_cast<v4f_f8*>(p + 16 * i) = y[i];
+        return;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < WN; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) m = max(m, __float_as_uint(y[i][v]) & 0x7FFFFFFFu);
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
+    if (row < 0 || n0 >= N) return;
+    // |y| * 2^-e in [1, 2) at the largest; a block with an infinity or NaN keeps them, and its finite values in range
+    const int e = m >= 0x7F800000u ? 113 : (m == 0 ? 0 : __builtin_amdgcn_frexp_expf(__uint_as_float(m)) - 1);
+    uint16_t* p = (uint16_t*)base + row * N + n0 + 4 * g;
+#pragma unroll
+    for (int i = 0; i < WN; ++i) {
+        uint32_t h[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) h[v] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_ldexpf(y[i][v], -e));
+        *reinterpret_cast<uint2*>(p + 16 * i) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    }
+    if (g == 0) scale[row * (N / kPairBlock) + n0 / kPairBlock] = __builtin_ldexpf(1.0f, e);
 }
 
 template <bool PP, int NWN, int NWM, int WN, int WM, int STAGES>
@@ -447,18 +483,14 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
             }
         }
     } else if constexpr (MODE == kFp8Down) {
-        const ElemType pt = a.pair_bf16 ? ElemType::kBF16 : ElemType::kF32;
         void* base = shared ? a.y_shared : a.y_pair;
+        float* scale = a.y_scale + (shared ? (int64_t)a.T * a.k * (a.N / kPairBlock) : 0);
 #pragma unroll
         for (int j = 0; j < WM; ++j) {
-            const int row = s_row[(wm * WM + j) * 16 + r16];
-            if (row < 0) continue;
+            v4f_f8 y[WN];
 #pragma unroll
-            for (int i = 0; i < WN; ++i) {
-                const int n = nb * C::NR + (wn * WN + i) * 16 + 4 * g;
-                const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                if (n < a.N) store4(base, (int64_t)row * a.N + n, pt, v, a.N - n, true);
-            }
+            for (int i = 0; i < WN; ++i) y[i] = acc[i][j];
+            store_row64<WN>(y, base, scale, a.pair16, s_row[(wm * WM + j) * 16 + r16], nb * C::NR + wn * WN * 16, a.N);
         }
     } else {
         constexpr int HI = WN / 2;
@@ -611,7 +643,8 @@ hipError_t launch_ffn_fp8(const Fp8FfnArgs& f, bool tiles_ready, hipStream_t s) 
     a.N = f.H;
     a.y_pair = f.y_pair;
     a.y_shared = f.y_shared;
-    a.pair_bf16 = f.pair_bf16;
+    a.y_scale = f.y_scale;
+    a.pair16 = f.pair16;
     a.nblocks = (f.H + 255) / 256;
     return f.exact ? launch_grouped<kFp8Down, true>(a, (int64_t)max_t * a.nblocks, s)
                    : launch_grouped<kFp8Down, false>(a, (int64_t)max_t * a.nblocks, s);
@@ -647,39 +680,46 @@ hipError_t launch_matmul_fp8(const Fp8MatmulArgs& m, hipStream_t s) {
 // ---------------------------------------------------------------------------
 namespace {
 
-__device__ __forceinline__ void load8_pair(const void* base, int bf16, int64_t idx, float (&v)[8]) {
-    if (bf16) {
-        const uint4 q = *reinterpret_cast<const uint4*>((const uint16_t*)base + idx);
-        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+__device__ __forceinline__ void load8_row(const void* base, const float* scale, int pair16, int64_t row, int o, int H,
+                                          float (&v)[8]) {
+    if (pair16) {
+        v8h_f8 q = *reinterpret_cast<const v8h_f8*>((const uint16_t*)base + row * H + o);
+        const float s = scale[row * (H / kPairBlock) + o / kPairBlock];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        }
+        for (int i = 0; i < 8; ++i) v[i] = (float)q[i] * s;
     } else {
-        const float4* p = reinterpret_cast<const float4*>((const float*)base + idx);
+        const float4* p = reinterpret_cast<const float4*>((const float*)base + row * H + o);
         const float4 a = p[0], b = p[1];
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
 }
 
 __global__ void __launch_bounds__(256) combine_fp8_kernel(const Fp8CombineArgs a) {
+    constexpr int kRows = 4;   // rows in flight
     const int H8 = a.H / 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= (int64_t)a.T * H8) return;
     const int64_t t = i / H8;
     const int o = (int)(i - t * H8) * 8;
     float acc[8] = {};
-    for (int j = 0; j < a.k; ++j) {
-        float v[8];
-        load8_pair(a.y_pair, a.pair_bf16, (t * a.k + j) * a.H + o, v);
-        const float w = a.w[t * a.k + j];
+    for (int j0 = 0; j0 < a.k; j0 += kRows) {
+        float v[kRows][8], w[kRows];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc[q] = fmaf(w, v[q], acc[q]);
+        for (int j = 0; j < kRows; ++j) {
+            const int64_t p = t * a.k + min(j0 + j, a.k - 1);
+            load8_row(a.y_pair, a.y_scale, a.pair16, p, o, a.H, v[j]);
+            w[j] = a.w[p];
+        }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            if (j0 + j >= a.k) break;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) acc[q] = fmaf(w[j], v[j][q], acc[q]);
+        }
     }
     if (a.y_shared) {
         float v[8];
-        load8_pair(a.y_shared, a.pair_bf16, t * a.H + o, v);
+        load8_row(a.y_shared, a.y_scale + (int64_t)a.T * a.k * (a.H / kPairBlock), a.pair16, t, o, a.H, v);
         const float w = a.shared_scale ? a.shared_scale[t] : 1.0f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) acc[q] = fmaf(w, v[q], acc[q]);

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kSkinnyThreads) skinny_down_kernel(const Fp8Ff
     constexpr int kCh = 4;
     __shared__ __attribute__((aligned(16))) unsigned char s_w[kSkinnyWaves][kCh * 2048];
     __shared__ __attribute__((aligned(16))) uint8_t s_q[kSkinnyWaves][kCh * kFp8Block];
-    __shared__ float s_y[kMaxSlots][16];
+    __shared__ float s_y[kMaxSlots][16], s_wt[kMaxSlots];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int r16 = lane & 15, g = lane >> 4;
@@ -279,6 +279,8 @@ __global__ void __launch_bounds__(kSkinnyThreads) skinny_down_kernel(const Fp8Ff
     const int ca = ((lane & 7) ^ (lane >> 3)) * 16;
     const int c0 = (g ^ (r16 & 7)) * 16, c1 = c0 ^ 64;
     const uint32_t l0 = lds_address(s_w[wave]);
+    if (c.out && tid < slots)   // the combine's weights, fetched beside the rows
+        s_wt[tid] = tid < f.k ? c.w[(int64_t)t * f.k + tid] : (c.shared_scale ? c.shared_scale[t] : 1.0f);
     for (int j = wave; j < slots; j += kSkinnyWaves) {
         const bool shared = j == f.k;
         Fp8Mat wd = shared ? f.sdown : f.down;
@@ -346,8 +348,7 @@ __global__ void __launch_bounds__(kSkinnyThreads) skinny_down_kernel(const Fp8Ff
     if (c.out) {
         if (tid < 16) {
             float s = 0.0f;
-            for (int j = 0; j < f.k; ++j) s = fmaf(c.w[(int64_t)t * f.k + j], s_y[j][tid], s);
-            if (f.has_shared) s = fmaf(c.shared_scale ? c.shared_scale[t] : 1.0f, s_y[f.k][tid], s);
+            for (int j = 0; j < slots; ++j) s = fmaf(s_wt[j], s_y[j][tid], s);
             const int64_t at = (int64_t)t * f.H + n0 + tid;
             if (c.ot == ElemType::kF32)
                 ((float*)c.out)[at] = s;

@@ -295,23 +295,22 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
             }
         } else {
             const int* pr = reinterpret_cast<const int*>(lds + C::kRing + 2 * C::kXs + cbuf * C::kMeta);
-            const ElemType pt = a.pair_bf16 ? ElemType::kBF16 : ElemType::kF32;
             void* base = ci.shared ? a.y_shared : a.y_pair;
+            float* scale = a.y_scale + (ci.shared ? (int64_t)P * (a.N / kPairBlock) : 0);
 #pragma unroll
             for (int j = 0; j < WM; ++j) {
                 const int m = (wm * WM + j) * 16 + r16;
-                const int row = ci.shared ? ci.mt0 + m : pr[m];
-                if (m >= ci.n_tok) continue;
-                if (!ci.shared && (uint32_t)row >= (uint32_t)P) {
+                int row = ci.shared ? ci.mt0 + m : pr[m];
+                if (m >= ci.n_tok) {
+                    row = -1;
+                } else if (!ci.shared && (uint32_t)row >= (uint32_t)P) {
                     raise_error(kErrPairRange);
-                    continue;
+                    row = -1;
                 }
+                v4f_f8 y[WN];
 #pragma unroll
-                for (int i = 0; i < WN; ++i) {
-                    const int n = ci.nb * C::NR + (wn * WN + i) * 16 + 4 * g;
-                    const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                    if (n < a.N) store4(base, (int64_t)row * a.N + n, pt, v, a.N - n, true);
-                }
+                for (int i = 0; i < WN; ++i) y[i] = acc[i][j];
+                store_row64<WN>(y, base, scale, a.pair16, row, ci.nb * C::NR + wn * WN * 16, a.N);
             }
         }
 #pragma unroll

@@ -291,8 +291,12 @@ def test_forward(T, E, k, H, I, shared, xt, flags):
     assert np.array_equal(r.idx.cpu().numpy(), idx)
     q, d = _quantize(m, x)
     y, dy, sh, dsh = _reference(host, _codes(q), d.cpu().numpy(), idx, fast=xt == "bf16")
-    pe = torch.finfo(torch.bfloat16).eps / 2 if flags else 0.0     # the per-pair hand-off's rounding
-    dy = dy * (1 + pe) + np.abs(y) * pe
+    def handed(v, dv):   # the 16-bit hand-off: fp16 times a power of two below twice the block's largest
+        if not flags:
+            return dv
+        big = np.repeat((np.abs(v) + dv).reshape(len(v), -1, 64).max(axis=2), 64, 1)
+        return dv + 2.0 ** -11 * (np.abs(v) + dv) + 2.0 ** -25 * big
+    dy = handed(y, dy)
     a = np.abs(w)[:, :, None]
     o = (w[:, :, None] * y.reshape(T, k, H)).sum(1)
     mag = (a * np.abs(y).reshape(T, k, H)).sum(1)
@@ -300,7 +304,7 @@ def test_forward(T, E, k, H, I, shared, xt, flags):
     if shared:
         s = sc.double().cpu().numpy()[:, None]
         o = o + s * sh
-        do += s * (dsh * (1 + pe) + np.abs(sh) * pe)
+        do += s * handed(sh, dsh)
         mag += s * np.abs(sh)
     do += (k + 3) * ref.U * (mag + do)                             # fp32 weights, k + 1 fmas
     half = 0 if xt == "f32" else torch.finfo(DT[xt]).eps / 2
