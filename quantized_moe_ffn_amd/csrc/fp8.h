@@ -175,10 +175,12 @@ __device__ __forceinline__ uint64_t wave_uniform(uint64_t v) {
 }
 // The same from a wave-uniform base and a 32-bit offset per lane.
 __device__ __forceinline__ void copy16_lds(uint64_t base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+                 "v"(off), "s"(wave_uniform(base)));
 }
 __device__ __forceinline__ void copy4_lds(uint64_t base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+                 "v"(off), "s"(wave_uniform(base)));
 }
 template <int N>
 __device__ __forceinline__ void wait_vm() {

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
             copy16_lds(ba[c < C::NA ? c : 0] + o, oa[c < C::NA ? c : 0], la + c * C::kWaves * 1024);
         else
             copy16_lds(bb + o, ob[c < C::NA ? 0 : c - C::NA], la + C::NR * 128 + (c - C::NA) * C::kWaves * 1024);
-        if (c == C::kLoads - 1 && (kb & 3) == 0)
+        if (c == C::kLoads - 1 && (kb & 3) == 0 && wave < C::kSegs)   // group 0's waves
             copy16_lds(bs + 4 * (uint64_t)kb, os, lds0 + C::kRing + ((kb >> 2) & 1) * C::MT * 16 + seg * 1024);
     };
     auto issue = [&](int kb) {
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
                 copy16_lds((const void*)(live ? bb + (d + ob[i]) : z), lb + i * C::kWaves * 1024);
         }
         if constexpr (PP) {
-            if ((kb & 3) == 0) copy16_lds(bs + 4 * (uint64_t)kb, os, lds0 + C::kRing + ((kb >> 2) & 1) * C::MT * 16 + seg * 1024);
+            if ((kb & 3) == 0 && wave < C::kSegs) copy16_lds(bs + 4 * (uint64_t)kb, os, lds0 + C::kRing + ((kb >> 2) & 1) * C::MT * 16 + seg * 1024);
         } else {
             copy4_lds(bs + 4 * (uint64_t)kb, os, st + (C::NR + C::MT) * 128 + seg * 256);
         }

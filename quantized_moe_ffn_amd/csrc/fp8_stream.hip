@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
         bs = wave_uniform((uint64_t)(a.xs + tok0 * KB));
 #pragma unroll
         for (int i = 0; i < C::NB; ++i) ob[i] = src((wave + i * C::kWaves) * 8 + lr) * (uint32_t)K + ca;
-        os = src(wave % C::kSegs * 64 + lane) * (uint32_t)KB * 4;
+        os = src(min(wave, C::kSegs - 1) * 64 + lane) * (uint32_t)KB * 4;
     };
 
     StreamItem cur = load_item(first), nxt = cur;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
     // were copied a whole item ago (K/128 >= STAGES blocks: older than the block just waited for).
     auto advance = [&]() {
         if ((ikb & 3) == 0) {
-            copy16_lds(wave_uniform(bs + 4 * (uint64_t)ikb), os, lds0 + C::kRing + ixs * C::kXs + wave % C::kSegs * 1024);
+            if (wave < C::kSegs) copy16_lds(wave_uniform(bs + 4 * (uint64_t)ikb), os, lds0 + C::kRing + ixs * C::kXs + wave * 1024);
             ixs ^= 1;
         }
         islot = islot + 1 == STAGES ? 0 : islot + 1;
@@ -213,9 +213,12 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
     const int c0 = (g ^ (r16 & 7)) * 16, c1 = c0 ^ 64;
     const unsigned char* la0 = lds + (wn * WN * 16 + r16) * 128 + c0;
     const unsigned char* la1 = lds + (wn * WN * 16 + r16) * 128 + c1;
-    const unsigned char* lb0 = lds + C::NR * 128 + (wm * WM * 16 + r16) * 128 + c0;
-    const unsigned char* lb1 = lds + C::NR * 128 + (wm * WM * 16 + r16) * 128 + c1;
-    const unsigned char* lsx = lds + C::kRing + (wm * WM * 16 + r16) * 16;
+    // a wave's token tile j is the item's tile j * NWM + wm, so that a part-filled item loads the waves alike;
+    // tiles past the item's last token are skipped (at 4,096 tokens a third of them)
+    auto tok = [&](int j) { return (j * NWM + wm) * 16 + r16; };
+    const unsigned char* lb0 = lds + C::NR * 128 + tok(0) * 128 + c0;
+    const unsigned char* lb1 = lds + C::NR * 128 + tok(0) * 128 + c1;
+    const unsigned char* lsx = lds + C::kRing + tok(0) * 16;
     v4f_f8 acc[WN][WM] = {};
     for (int s = 0; s < total; ++s) {
         if (s + STAGES - 2 < total)
@@ -227,22 +230,26 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
         const float* pw = reinterpret_cast<const float*>(lds + C::kRing + 2 * C::kXs + cbuf * C::kMeta + C::kTok * 4);
         // down: 256 rows are two scale blocks, four waves of 64 rows
         const float wb0 = pw[(kGu ? 0 : (wn >> 1) * 64) + kb], wb1 = kGu ? pw[64 + kb] : 0.f;
+        const int nj = (ci.n_tok + 15) / 16 - wm;   // token tiles j * NWM + wm of this wave
         Fp8Frag<EXACT> fa[WN];
 #pragma unroll
         for (int i = 0; i < WN; ++i)
             fa[i].set(*reinterpret_cast<const int4*>(la0 + st + i * 2048), *reinterpret_cast<const int4*>(la1 + st + i * 2048));
 #pragma unroll
         for (int j = 0; j < WM; ++j) {
-            Fp8Frag<EXACT> fb;
-            fb.set(*reinterpret_cast<const int4*>(lb0 + st + j * 2048), *reinterpret_cast<const int4*>(lb1 + st + j * 2048));
-            const float x = *reinterpret_cast<const float*>(lsx + xs + j * 256 + (kb & 3) * 4);
-            const float s0 = x * wb0, s1 = kGu ? x * wb1 : 0.f;
+            if (j * NWM < nj) {
+                Fp8Frag<EXACT> fb;
+                fb.set(*reinterpret_cast<const int4*>(lb0 + st + j * NWM * 2048),
+                       *reinterpret_cast<const int4*>(lb1 + st + j * NWM * 2048));
+                const float x = *reinterpret_cast<const float*>(lsx + xs + j * NWM * 256 + (kb & 3) * 4);
+                const float s0 = x * wb0, s1 = kGu ? x * wb1 : 0.f;
 #pragma unroll
-            for (int i = 0; i < WN; ++i) {
-                const v4f_f8 t = fa[i].times(fb);
-                const float sc = kGu && i >= WN / 2 ? s1 : s0;
+                for (int i = 0; i < WN; ++i) {
+                    const v4f_f8 t = fa[i].times(fb);
+                    const float sc = kGu && i >= WN / 2 ? s1 : s0;
 #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(t[v], sc, acc[i][j][v]);
+                    for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(t[v], sc, acc[i][j][v]);
+                }
             }
             if (more) {
 #pragma unroll
@@ -254,7 +261,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
         if ((kb & 3) == 3) xs ^= C::kXs;
         if (++kb < KB) continue;
 
-        // The item's results: value v of acc[i][j] is weight row 16*i + 4*g + v, token 16*j + r16 of the wave.
+        // The item's results: value v of acc[i][j] is weight row 16*i + 4*g + v of the wave, token tok(j).
         // The copies of the next item's first blocks are in flight.
         if constexpr (kGu) {
             constexpr int HI = WN / 2;
@@ -271,13 +278,13 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
                     }
                 mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, kWave));
                 mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, kWave));
-                if (g == 0) s_amax[wn][(wm * WM + j) * 16 + r16] = mx;
+                if (g == 0) s_amax[wn][tok(j)] = mx;
             }
             lds_barrier();
             const int64_t row0 = (int64_t)ci.off + ci.mt0;
 #pragma unroll
             for (int j = 0; j < WM; ++j) {
-                const int m = (wm * WM + j) * 16 + r16;
+                const int m = tok(j);
                 uint32_t mx = s_amax[0][m];
 #pragma unroll
                 for (int q = 1; q < NWN; ++q) mx = max(mx, s_amax[q][m]);
@@ -299,7 +306,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
             float* scale = a.y_scale + (ci.shared ? (int64_t)P * (a.N / kPairBlock) : 0);
 #pragma unroll
             for (int j = 0; j < WM; ++j) {
-                const int m = (wm * WM + j) * 16 + r16;
+                const int m = tok(j);
                 int row = ci.shared ? ci.mt0 + m : pr[m];
                 if (m >= ci.n_tok) {
                     row = -1;
