@@ -44,11 +44,26 @@ struct Fp8Mat {
 hipError_t launch_quantize_fp8(const void* x, ElemType xt, int64_t ldx, int T, int H, uint8_t* xq, float* xs,
                                hipStream_t s);
 
+// The grouped products' work list: tile i of expert e covers rows mt*i .. of its
+// bucket; the shared expert's tiles (e = E) cover all T tokens.  row0 is the
+// tile's first row of h: its position in the bucket order, or T*k + m0.
+struct Fp8Item {
+    int e, m0, n_tok, row0;
+};
+struct Fp8ItemList {
+    Fp8Item* items;
+    int32_t* n_items;
+    int mt;                  // tokens per tile; 0: no list
+    int max_items;
+    int T;
+    int has_shared;
+};
+
 // A layer call's routing: launch_route_scored, x [T][H] quantised by extra workgroups of the same launch and, with
-// tl.mt > 0, the grouped products' work list (TileList, kernels.h).
+// tl.mt > 0, the grouped products' work list; *list_done says whether that was written.
 hipError_t launch_route_quantize_fp8(const float* logits, int T, int E, int k, const ScoreRule& rule,
-                                     const RoutingPtrs& r, void* ws, const TileList& tl, const void* x, ElemType xt, int H,
-                                     uint8_t* xq, float* xs, hipStream_t s);
+                                     const RoutingPtrs& r, void* ws, const Fp8ItemList& tl, const void* x, ElemType xt, int H,
+                                     uint8_t* xq, float* xs, hipStream_t s, bool* list_done);
 
 struct Fp8MatmulArgs {
     const uint8_t* xq;
@@ -74,12 +89,12 @@ struct Fp8FfnArgs {
     float* y_scale;          // pair16: [T*k (+T)][H/64]
     int pair16;
     int exact;               // products with fp32 sums throughout (fp8_gemm.hip)
-    int32_t* tiles;          // workspace: the work list (fp8_tiles_bytes)
+    void* tiles;             // workspace: the work list (fp8_items_bytes), 16-byte aligned
     float* hf;               // workspace of the few-pair kernels: h in fp32, [T*k (+T)][I]
 };
-size_t fp8_tiles_bytes(int T, int k, int E, int has_shared);
-TileList fp8_tile_list(const Fp8FfnArgs& f);   // the list launch_ffn_fp8 works through, in f.tiles
-hipError_t launch_ffn_fp8(const Fp8FfnArgs& a, bool tiles_ready, hipStream_t s);
+size_t fp8_items_bytes(int T, int k, int E, int has_shared);
+Fp8ItemList fp8_item_list(const Fp8FfnArgs& f);   // the list launch_ffn_fp8 works through, in f.tiles
+hipError_t launch_ffn_fp8(const Fp8FfnArgs& a, bool list_done, hipStream_t s);
 
 // Few pairs: T*k up to this, and up to the expert count, so that few pairs share an expert's read.
 constexpr int kFewPairs = 64;

@@ -121,7 +121,7 @@ Fp8FfnWorkspace fp8_ffn_layout(const moe_fp8_layer* L, int T, int k) {
     w.hs = off;
     off += align_up(rows * (L->inter / MOE_FP8_BLOCK) * sizeof(float), 256);
     w.tiles = off;
-    off += align_up(moe::fp8_tiles_bytes(T, k, L->n_experts, L->has_shared ? 1 : 0), 256);
+    off += align_up(moe::fp8_items_bytes(T, k, L->n_experts, L->has_shared ? 1 : 0), 256);
     w.total = off;
     return w;
 }
@@ -177,7 +177,7 @@ moe::Fp8FfnArgs fp8_ffn_args(const moe_fp8_layer* L, const moe_routing* r, int T
     a.r = moe::RoutingPtrs{r->idx, r->w, r->count, r->offset, r->pair, r->active, r->n_active};
     a.hq = (uint8_t*)(ws + w.hq);
     a.hs = (float*)(ws + w.hs);
-    a.tiles = (int32_t*)(ws + w.tiles);
+    a.tiles = ws + w.tiles;
     a.hf = (float*)(ws + w.hf);
     return a;
 }
@@ -306,15 +306,17 @@ moe_status moe_forward_fp8(const moe_fp8_layer* L, const moe_route_spec* spec, c
     a.pair16 = pair16 ? 1 : 0;
     a.exact = xt == moe::ElemType::kBF16 ? 0 : 1;
     const bool few = moe::fp8_few_pairs(T, k, L->n_experts);
-    const moe::TileList tl = few ? moe::TileList{} : moe::fp8_tile_list(a);
+    const moe::Fp8ItemList tl = few ? moe::Fp8ItemList{} : moe::fp8_item_list(a);
+    bool list_done = false;
     hipError_t e = moe::launch_route_quantize_fp8(logits, T, L->n_experts, k, to_rule(*spec), a.r, ws + wl.route, tl, x, xt,
-                                                  L->hidden, (uint8_t*)(ws + wl.xq), (float*)(ws + wl.xs), stream);
+                                                  L->hidden, (uint8_t*)(ws + wl.xq), (float*)(ws + wl.xs), stream,
+                                                  &list_done);
     if (e != hipSuccess) return from_hip(e, "moe_forward_fp8: routing and quantisation launch");
     const moe::Fp8CombineArgs c{a.y_pair, a.y_shared, a.y_scale, a.pair16, r->w, shared_scale, out, xt, T, k, L->hidden};
     if (few)
         return finish(from_hip(moe::launch_skinny_ffn(a, c, stream), "moe_forward_fp8: expert FFN launch"), stream,
                       "moe_forward_fp8");
-    e = moe::launch_ffn_fp8(a, true, stream);
+    e = moe::launch_ffn_fp8(a, list_done, stream);
     if (e != hipSuccess) return from_hip(e, "moe_forward_fp8: expert FFN launch");
     return finish(from_hip(moe::launch_combine_fp8(c, stream), "moe_forward_fp8: combine launch"), stream,
                   "moe_forward_fp8");

@@ -56,8 +56,8 @@ struct Fp8TileArgs {
     int vec_ok;                // 4-value stores are aligned
     int n_mt;                  // token tiles
     // grouped
-    const int32_t *count, *offset, *pair;
-    TileList tl;
+    const int32_t* pair;
+    Fp8ItemList tl;
     uint8_t* hq;               // gate/up: out
     float* hs;
     void* y_pair;              // down: out
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
 
     // the work item: weights, row block, tokens
     Fp8Mat m0 = a.w0, m1 = a.w1;
-    int nb, mt0, n_tok, e = 0, off = 0;
+    int nb, mt0, n_tok, e = 0, off = 0;   // off: the item's first row of h
     bool shared = false;
     if constexpr (MODE == kFp8Dense) {
         // XCD x takes a contiguous range of items; inside it, bands of 8 row blocks
@@ -178,26 +178,21 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
         mt0 = (in / width) * C::MT;
         n_tok = min(C::MT, a.T - mt0);
     } else {
-        const int n_work = __builtin_amdgcn_readfirstlane(*a.tl.n_tiles) * a.nblocks;
+        const int n_work = __builtin_amdgcn_readfirstlane(*a.tl.n_items) * a.nblocks;
         const int chunk = (n_work + 7) / 8;
         const int w = (blockIdx.x % 8) * chunk + blockIdx.x / 8;
         if ((int)(blockIdx.x / 8) >= chunk || w >= n_work) return;
         const int u = w / a.nblocks;
         nb = w - u * a.nblocks;
-        e = __builtin_amdgcn_readfirstlane(a.tl.tile_e[u]);
-        mt0 = __builtin_amdgcn_readfirstlane(a.tl.tile_m0[u]);
+        e = __builtin_amdgcn_readfirstlane(a.tl.items[u].e);
+        mt0 = __builtin_amdgcn_readfirstlane(a.tl.items[u].m0);
+        n_tok = __builtin_amdgcn_readfirstlane(a.tl.items[u].n_tok);
+        off = __builtin_amdgcn_readfirstlane(a.tl.items[u].row0);
         shared = e >= a.E;
-        int c = a.T;
         if (shared) {
             m0 = a.s0;
             m1 = a.s1;
         } else {
-            c = __builtin_amdgcn_readfirstlane(a.count[e]);
-            off = __builtin_amdgcn_readfirstlane(a.offset[e]);
-            if (c < 0 || off < 0 || (int64_t)off + c > (int64_t)a.T * a.k) {   // buffers not from a routing pass
-                if (tid == 0) raise_error(kErrPairRange);
-                return;
-            }
             m0.data += (int64_t)e * m0.expert_stride;
             m0.scale += (int64_t)e * ((m0.rows + 127) / 128) * KB;
             if constexpr (MODE == kFp8GateUp) {
@@ -205,11 +200,10 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
                 m1.scale += (int64_t)e * ((m1.rows + 127) / 128) * KB;
             }
         }
-        n_tok = min(C::MT, c - mt0);
         for (int m = tid; m < C::MT; m += C::kThreads) {
             int row = -1;
             if (m < n_tok) {
-                row = shared ? mt0 + m : a.pair[off + mt0 + m];
+                row = shared ? mt0 + m : a.pair[off + m];
                 if (!shared && (uint32_t)row >= (uint32_t)(a.T * a.k)) {
                     raise_error(kErrPairRange);
                     row = -1;
@@ -241,7 +235,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
             oa[i] = (uint32_t)((min(nb * C::NR + R8 + lr, a.N - 1) - first) * (int)m0.row_stride + ca);
         }
     }
-    const int64_t tok0 = MODE == kFp8Dense ? mt0 : (MODE == kFp8Down ? (shared ? (int64_t)a.T * a.k : (int64_t)off) + mt0 : 0);
+    const int64_t tok0 = MODE == kFp8Dense ? mt0 : (MODE == kFp8Down ? off : 0);
     const uint64_t bb = wave_uniform((uint64_t)(a.xq + tok0 * K));
     // token of the tile's row m from tok0 on (a valid one past the end)
     auto src_row = [&](int m) -> uint32_t {
@@ -511,7 +505,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
             if (g == 0) s_amax[wn][(wm * WM + j) * 16 + r16] = mx;
         }
         __syncthreads();
-        const int64_t row0 = (shared ? (int64_t)a.T * a.k : (int64_t)off) + mt0;
+        const int64_t row0 = off;
 #pragma unroll
         for (int j = 0; j < WM; ++j) {
             const int m = (wm * WM + j) * 16 + r16;
@@ -543,12 +537,19 @@ namespace moe {
 
 namespace {
 
-// The work list of the grouped products from the bucket counts.
-__global__ void __launch_bounds__(1024) fp8_tiles_kernel(const int32_t* count, int npairs, int E, TileList tl) {
+// The work list from the buckets of a routing call.  A count or offset outside
+// its range cannot come from one: it raises kErrPairRange and gives no items.
+__global__ void __launch_bounds__(1024) fp8_items_kernel(const int32_t* count, const int32_t* offset, int npairs, int E,
+                                                         Fp8ItemList tl) {
     __shared__ int s_wave[kWave + 1];
-    __shared__ int s_start[1024];
+    __shared__ int s_start[1024], s_cnt[1024], s_off[1024];
     const int tid = threadIdx.x;
-    write_tile_list(tid < E ? count[tid] : 0, npairs, E, tl, s_wave, s_start);
+    int c = tid < E ? count[tid] : 0, off = tid < E ? offset[tid] : 0;
+    if (c < 0 || off < 0 || (int64_t)off + c > npairs) {
+        raise_error(kErrPairRange);
+        c = off = 0;
+    }
+    write_item_list(c, off, npairs, E, tl, s_wave, s_start, s_cnt, s_off);
 }
 
 template <int MODE, bool EXACT, bool PP, int NWN, int NWM, int WN, int WM, int STAGES>
@@ -593,26 +594,25 @@ hipError_t launch_dense(const Fp8TileArgs& a, int mt, int64_t n_work, hipStream_
 
 }  // namespace
 
-size_t fp8_tiles_bytes(int T, int k, int E, int has_shared) {
-    return (size_t)(2 * (int64_t)fp8_max_tiles(T, k, E, has_shared, fp8_tile_tokens(T, k, E)) + 1) * sizeof(int32_t);
+size_t fp8_items_bytes(int T, int k, int E, int has_shared) {
+    return (size_t)fp8_max_tiles(T, k, E, has_shared, fp8_tile_tokens(T, k, E)) * sizeof(Fp8Item) + 16;
 }
 
-TileList fp8_tile_list(const Fp8FfnArgs& f) {
-    TileList tl{};
+Fp8ItemList fp8_item_list(const Fp8FfnArgs& f) {
+    Fp8ItemList tl{};
     tl.mt = fp8_tile_tokens(f.T, f.k, f.E);
-    tl.max_t = fp8_max_tiles(f.T, f.k, f.E, f.has_shared, tl.mt);
-    tl.tile_e = f.tiles;
-    tl.tile_m0 = f.tiles + tl.max_t;
-    tl.n_tiles = f.tiles + 2 * (int64_t)tl.max_t;
+    tl.max_items = fp8_max_tiles(f.T, f.k, f.E, f.has_shared, tl.mt);
+    tl.n_items = (int32_t*)f.tiles;
+    tl.items = (Fp8Item*)((char*)f.tiles + 16);
     tl.T = f.T;
     tl.has_shared = f.has_shared;
     return tl;
 }
 
-hipError_t launch_ffn_fp8(const Fp8FfnArgs& f, bool tiles_ready, hipStream_t s) {
-    const TileList tl = fp8_tile_list(f);
-    const int max_t = tl.max_t;
-    if (!tiles_ready) fp8_tiles_kernel<<<1, 1024, 0, s>>>(f.r.count, f.T * f.k, f.E, tl);
+hipError_t launch_ffn_fp8(const Fp8FfnArgs& f, bool list_done, hipStream_t s) {
+    const Fp8ItemList tl = fp8_item_list(f);
+    const int max_t = tl.max_items;
+    if (!list_done) fp8_items_kernel<<<1, 1024, 0, s>>>(f.r.count, f.r.offset, f.T * f.k, f.E, tl);
     Fp8TileArgs a{};
     a.w0 = f.gate;
     a.w1 = f.up;
@@ -625,8 +625,6 @@ hipError_t launch_ffn_fp8(const Fp8FfnArgs& f, bool tiles_ready, hipStream_t s) 
     a.T = f.T;
     a.k = f.k;
     a.E = f.E;
-    a.count = f.r.count;
-    a.offset = f.r.offset;
     a.pair = f.r.pair;
     a.tl = tl;
     a.hq = f.hq;

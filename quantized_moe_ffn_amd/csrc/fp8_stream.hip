@@ -10,9 +10,9 @@
 // list (item: 256 weight rows x one token tile; the row blocks of a tile are
 // neighbours, so workgroups that run at once share tokens and weights in L2),
 // and the copies run STAGES - 1 blocks ahead across item borders.  An item's
-// list entry, pair ids and weight scales are fetched one item ahead: the entry
-// by scalar loads, the rest by copies to LDS, so that the main loop holds no
-// load the compiler would wait for (its wait would drain the copies too).
+// pair ids and weight scales are copied to LDS one item ahead, its list entry
+// two, so that the main loop holds no load the compiler would wait for (its
+// wait would drain the copies too).
 //
 // Needs K a multiple of 512 (token scales are copied four blocks at a time) and
 // at most 8,192 (the 64 weight scales of an item are one copy).
@@ -25,18 +25,9 @@ namespace {
 constexpr int kStreamMaxK = 64 * kFp8Block;
 inline bool fp8_stream_k(int K) { return K % (4 * kFp8Block) == 0 && K <= kStreamMaxK; }
 
-// Two words by scalar loads, waited for here.
-__device__ __forceinline__ void scalar_load2(const int32_t* p, const int32_t* q, int& a, int& b) {
-    asm volatile("s_load_dword %0, %2, 0x0\n\ts_load_dword %1, %3, 0x0\n\ts_waitcnt lgkmcnt(0)"
-                 : "=&s"(a), "=&s"(b)
-                 : "s"(wave_uniform((uint64_t)p)), "s"(wave_uniform((uint64_t)q))
-                 : "memory");
-}
-
-// One work item, the same in every lane.  n_tok = 0: its bucket is not one a
-// routing pass leaves (the copies then read row 0 and nothing is stored).
+// One work item (row block nb of list entry e, m0, n_tok, row0), the same in every lane.
 struct StreamItem {
-    int e, nb, mt0, n_tok, off;
+    int e, nb, mt0, n_tok, row0;
     bool shared;
 };
 
@@ -51,7 +42,8 @@ struct StreamShape {
     static constexpr int kStage = (NR + MT) * 128, kRing = STAGES * kStage;
     static constexpr int kXs = kTok * 16;             // token scales: [token][4 blocks], two buffers
     static constexpr int kMeta = kTok * 4 + 512;      // an item's pair ids and 2 x 64 weight scales, three buffers
-    static constexpr int kLds = kRing + 2 * kXs + 3 * kMeta;
+    static constexpr int kEntry = kRing + 2 * kXs + 3 * kMeta;   // list entries: 64 words each (a copy's size), two buffers
+    static constexpr int kLds = kEntry + 512;
     static_assert(NA * 8 * kWaves == NR && NB * 8 * kWaves == MT && NR == 256, "copies divide evenly");
     static_assert(kWaves >= kSegs + 2 && kLds + NWN * MT * 4 <= 160 * 1024 && STAGES <= 4, "shape");
 };
@@ -69,46 +61,41 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
     const int K = a.K, KB = K / kFp8Block, P = a.T * a.k;
     const uint32_t lds0 = lds_address(lds);
 
-    int n_tiles, unused;
-    scalar_load2(a.tl.n_tiles, a.tl.n_tiles, n_tiles, unused);
-    const int n_work = n_tiles * a.nblocks;
+    const int n_work = __builtin_amdgcn_readfirstlane(*a.tl.n_items) * a.nblocks;
     const int chunk = (n_work + 7) / 8, step = gridDim.x / 8;
     const int first = (blockIdx.x % 8) * chunk + blockIdx.x / 8;
     const int lim = min((int)(blockIdx.x % 8 + 1) * chunk, n_work);
     if (first >= lim) return;
     const int total = ((lim - first - 1) / step + 1) * KB;   // stages of this workgroup
 
-    auto load_item = [&](int w) {
+    // Copies item w's list entry into buffer b (wave 0); reads the one copied there.
+    auto fetch_entry = [&](int w, int b) {
+        if (wave == 0) copy4_lds((uint64_t)(a.tl.items + w / a.nblocks), (uint32_t)(lane & 3) * 4, lds0 + C::kEntry + b * 256);
+    };
+    auto read_entry = [&](int w, int b) {
+        const int4 v = *reinterpret_cast<const int4*>(lds + C::kEntry + b * 256);
         StreamItem it;
-        const int u = w / a.nblocks;
-        it.nb = w - u * a.nblocks;
-        scalar_load2(a.tl.tile_e + u, a.tl.tile_m0 + u, it.e, it.mt0);
+        it.nb = w % a.nblocks;
+        it.e = __builtin_amdgcn_readfirstlane(v.x);
+        it.mt0 = __builtin_amdgcn_readfirstlane(v.y);
+        it.n_tok = __builtin_amdgcn_readfirstlane(v.z);
+        it.row0 = __builtin_amdgcn_readfirstlane(v.w);
         it.shared = it.e >= a.E;
-        int c = a.T;
-        it.off = P;   // the shared expert's rows of h follow the pairs'
-        if (!it.shared) {
-            scalar_load2(a.count + it.e, a.offset + it.e, c, it.off);
-            if (c < 0 || it.off < 0 || (int64_t)it.off + c > P) {   // buffers not from a routing pass
-                if (tid == 0) raise_error(kErrPairRange);
-                c = it.off = it.mt0 = 0;
-            }
-        }
-        it.n_tok = max(0, min(C::MT, c - it.mt0));
         return it;
     };
     // Copies of an item's pair ids and weight scales into buffer b.
     auto fetch_meta = [&](const StreamItem& it, int b) {
         const uint32_t at = lds0 + C::kRing + 2 * C::kXs + b * C::kMeta;
         if (wave < C::kSegs) {
-            const int m = min(wave * 64 + lane, max(it.n_tok, 1) - 1);
+            const int m = min(wave * 64 + lane, it.n_tok - 1);
             if (!it.shared)
-                copy4_lds(wave_uniform((uint64_t)(a.pair + it.off + it.mt0)), (uint32_t)m * 4, at + wave * 256);
+                copy4_lds((uint64_t)(a.pair + it.row0), (uint32_t)m * 4, at + wave * 256);
         } else if (wave < C::kSegs + 2) {
             const int q = wave - C::kSegs;
             const int sb = kGu ? it.nb : min(2 * it.nb + q, (a.N - 1) / kFp8Block);
             const float* sc = kGu && q ? (it.shared ? a.s1.scale : a.w1.scale) : (it.shared ? a.s0.scale : a.w0.scale);
             const int64_t rb = it.shared ? 0 : (int64_t)it.e * ((a.N + kFp8Block - 1) / kFp8Block);
-            copy4_lds(wave_uniform((uint64_t)(sc + (rb + sb) * KB)), (uint32_t)min(lane, KB - 1) * 4,
+            copy4_lds((uint64_t)(sc + (rb + sb) * KB), (uint32_t)min(lane, KB - 1) * 4,
                       at + C::kTok * 4 + q * 256);
         }
     };
@@ -139,7 +126,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
             }
         }
         // token operand: gate/up gathers rows of x, down reads the bucket's rows of h
-        const int last = max(it.n_tok, 1) - 1;
+        const int last = it.n_tok - 1;
         auto src = [&](int m) -> uint32_t {
             m = min(m, last);
             if constexpr (!kGu) return m;
@@ -148,7 +135,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
             if (p >= (uint32_t)P) raise_error(kErrPairRange);
             return p < (uint32_t)P ? p / (uint32_t)a.k : 0u;
         };
-        const int64_t tok0 = kGu ? 0 : (int64_t)it.off + it.mt0;
+        const int64_t tok0 = kGu ? 0 : it.row0;
         bb = wave_uniform((uint64_t)(a.xq + tok0 * K));
         bs = wave_uniform((uint64_t)(a.xs + tok0 * KB));
 #pragma unroll
@@ -156,15 +143,19 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
         os = src(min(wave, C::kSegs - 1) * 64 + lane) * (uint32_t)KB * 4;
     };
 
-    StreamItem cur = load_item(first), nxt = cur;
-    int iw = first, ikb = 0, islot = 0, ixs = 0, ibuf = 0;   // item, block, ring slot, scale and meta buffer of the copies
+    int iw = first, ikb = 0, islot = 0, ixs = 0, ibuf = 0, ient = 0;   // the copies' item, block, ring slot and buffers
+    fetch_entry(first, 0);
+    fetch_entry(min(first + step, lim - 1), 1);
+    wait_vm<0>();
+    lds_barrier();
+    StreamItem cur = read_entry(first, 0), nxt = read_entry(min(first + step, lim - 1), 1);
     fetch_meta(cur, 0);
     wait_vm<0>();
     lds_barrier();
     setup(cur, 0);
     if (first + step < lim) {
-        nxt = load_item(first + step);
         fetch_meta(nxt, 1);
+        if (first + 2 * step < lim) fetch_entry(first + 2 * step, 0);
     }
     // Copy c of the next block (kLoads of them, then possibly the token scales).  They go out between the
     // MFMAs: the address unit takes about 16 cycles for each, 768 a block, which would otherwise stand
@@ -178,7 +169,8 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
             copy16_lds(bb + o, ob[c < C::NA ? 0 : c - C::NA], la + C::NR * 128 + (c - C::NA) * C::kWaves * 1024);
     };
     // After the copies: moves on to the next block; past an item's last one to the next item, whose pair ids
-    // were copied a whole item ago (K/128 >= STAGES blocks: older than the block just waited for).
+    // (and the entry after it) were copied a whole item ago (K/128 > STAGES blocks: older than the block just
+    // waited for).
     auto advance = [&]() {
         if ((ikb & 3) == 0) {
             if (wave < C::kSegs) copy16_lds(wave_uniform(bs + 4 * (uint64_t)ikb), os, lds0 + C::kRing + ixs * C::kXs + wave * 1024);
@@ -193,8 +185,10 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
                 cur = nxt;
                 setup(cur, ibuf);
                 if (iw + step < lim) {
-                    nxt = load_item(iw + step);
+                    nxt = read_entry(iw + step, ient);
+                    ient ^= 1;
                     fetch_meta(nxt, ibuf == 2 ? 0 : ibuf + 1);
+                    if (iw + 2 * step < lim) fetch_entry(iw + 2 * step, ient);
                 }
             }
         }
@@ -281,7 +275,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
                 if (g == 0) s_amax[wn][tok(j)] = mx;
             }
             lds_barrier();
-            const int64_t row0 = (int64_t)ci.off + ci.mt0;
+            const int64_t row0 = ci.row0;
 #pragma unroll
             for (int j = 0; j < WM; ++j) {
                 const int m = tok(j);

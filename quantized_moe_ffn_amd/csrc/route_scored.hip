@@ -274,14 +274,61 @@ __device__ __forceinline__ void wave_topk_scored(const float* __restrict__ lg, i
     out_w = (float)(w * (double)rule.scale);
 }
 
+// The grouped products' work list from the bucket counts and offsets (Fp8ItemList,
+// fp8.h).  Every thread of the workgroup calls it (blockDim.x >= E); thread e < E
+// passes expert e's, the others 0.  s_start, s_cnt, s_off: E ints of LDS each.
+// A thread finds entry j's expert as the last one whose first entry is <= j
+// (experts without tiles share the next one's first entry).
+__device__ void write_item_list(int c, int off, int npairs, int E, const Fp8ItemList& tl, int* s_wave, int* s_start,
+                                int* s_cnt, int* s_off) {
+    const int tid = threadIdx.x;
+    int total = 0;
+    const int start = block_exclusive_scan((c + tl.mt - 1) / tl.mt, s_wave, total);
+    if (tid < E) {
+        s_start[tid] = start;
+        s_cnt[tid] = c;
+        s_off[tid] = off;
+    }
+    __syncthreads();
+    const int ns = tl.has_shared ? (tl.T + tl.mt - 1) / tl.mt : 0;
+    const int n = min(total + ns, tl.max_items);   // counts of a routing pass never exceed it
+    for (int j = tid; j < n; j += blockDim.x) {
+        Fp8Item it;
+        if (j < total) {
+            int lo = 0, hi = E - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (s_start[mid] <= j)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            it.e = lo;
+            it.m0 = (j - s_start[lo]) * tl.mt;
+            it.n_tok = min(tl.mt, s_cnt[lo] - it.m0);
+            it.row0 = s_off[lo] + it.m0;
+        } else {
+            it.e = E;
+            it.m0 = (j - total) * tl.mt;
+            it.n_tok = min(tl.mt, tl.T - it.m0);
+            it.row0 = npairs + it.m0;
+        }
+        *reinterpret_cast<int4*>(tl.items + j) = make_int4(it.e, it.m0, it.n_tok, it.row0);
+    }
+    if (tid == 0) {
+        if (total + ns > tl.max_items) raise_error(kErrPairRange);
+        *tl.n_items = n;
+    }
+}
+
 // T*k <= kSmallPairs: workgroup 0 routes and buckets, the others quantise x (layer call).
 template <int V, typename XT>
 __global__ void __launch_bounds__(1024) route_scored_small_kernel(const float* __restrict__ logits, int T, int E, int k,
-                                                                  ScoreRule rule, RoutingPtrs r, int waves, TileList tl,
+                                                                  ScoreRule rule, RoutingPtrs r, int waves, Fp8ItemList tl,
                                                                   ActQuant<XT> aq) {
     extern __shared__ double s_buf[];               // [waves][E], then mask[E][words]: a bit per token that chose e
     __shared__ __attribute__((aligned(16))) int s_idx[kSmallPairs];
-    __shared__ int s_off[1024];
+    __shared__ int s_off[1024], s_cnt[1024], s_start[1024];
     __shared__ int s_wave[kWave + 1];
     if (blockIdx.x > 0) {
         aq.run(blockIdx.x - 1);
@@ -362,7 +409,7 @@ __global__ void __launch_bounds__(1024) route_scored_small_kernel(const float* _
     }
     if (tl.mt > 0) {
         __syncthreads();   // s_off is free again
-        write_tile_list(c, P, E, tl, s_wave, s_off);
+        write_item_list(c, pre & 0xFFFF, P, E, tl, s_wave, s_start, s_cnt, s_off);
     }
 }
 
@@ -418,9 +465,9 @@ __global__ void __launch_bounds__(1024) route_scored_tile_kernel(const float* __
 __global__ void __launch_bounds__(1024) route_place_kernel(const int32_t* __restrict__ idx, int T, int E, int k, int tt,
                                                            int n_tiles, int per, const uint8_t* __restrict__ hist,
                                                            const uint8_t* __restrict__ rank, int hist_ld,
-                                                           RoutingPtrs r, TileList tl) {
+                                                           RoutingPtrs r, Fp8ItemList tl) {
     __shared__ uint32_t s_sum[2][1024];   // [before | all][expert]
-    __shared__ int s_base[1024];
+    __shared__ int s_base[1024], s_list[1024];
     __shared__ int s_wave[kWave + 1];
     const int tid = threadIdx.x;
     const int cols = hist_ld / 4;
@@ -470,7 +517,9 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const int32_t* __rest
             r.offset[E] = total;
             *r.n_active = n_act;
         }
-        if (tl.mt > 0) write_tile_list(cnt, T * k, E, tl, s_wave, reinterpret_cast<int*>(s_sum[0]));
+        if (tl.mt > 0)
+            write_item_list(cnt, off, T * k, E, tl, s_wave, reinterpret_cast<int*>(s_sum[0]),
+                            reinterpret_cast<int*>(s_sum[1]), s_list);
     }
     __syncthreads();
     for (int tile = first; tile < min(first + per, n_tiles); ++tile) {
@@ -504,7 +553,7 @@ __global__ void __launch_bounds__(256) route_scored_tokens_kernel(const float* _
 // The layer call's part of the routing launches: x to quantise (null: none) and the work list (mt 0: none).
 template <int V, typename XT>
 hipError_t route_scored_v(const float* logits, int T, int E, int k, const ScoreRule& rule, const RoutingPtrs& r,
-                          void* ws, hipStream_t s, const TileList& tl, const ActQuant<XT>& aq) {
+                          void* ws, hipStream_t s, const Fp8ItemList& tl, const ActQuant<XT>& aq) {
     const int P = T * k;
     const unsigned nq = aq.x ? aq.groups() : 0;
     // one wave's score buffer is E doubles: at most 64 KB of them in a workgroup
@@ -523,9 +572,9 @@ hipError_t route_scored_v(const float* logits, int T, int E, int k, const ScoreR
                                                                                              r.idx, r.w);
         if (aq.x) quantize_fp8_kernel<XT><<<nq, 1024, 0, s>>>(aq);
         bucket_tile_kernel<<<n_tiles, kTilePairs, 0, s>>>(r.idx, P, E, tile_hist, rank);
-        bucket_scan_kernel<<<1, 1024, 0, s>>>(n_tiles, E, P, tile_hist, r, tl);
+        bucket_scan_kernel<<<1, 1024, 0, s>>>(n_tiles, E, P, tile_hist, r, TileList{});
         bucket_scatter_kernel<<<(P + 255) / 256, 256, 0, s>>>(r.idx, P, E, tile_hist, r.offset, rank, r.pair);
-        return hipGetLastError();
+        return hipGetLastError();   // the work list is left to launch_ffn_fp8
     }
     // 64-token tiles for k < 4 keep the counts within route_workspace_bytes: ceil(T/64) * E bytes there,
     // ceil(T/16) * E <= ceil(T*k/256) * E * 4 for k >= 4
@@ -547,7 +596,7 @@ hipError_t route_scored_v(const float* logits, int T, int E, int k, const ScoreR
 
 template <typename XT>
 hipError_t route_scored_x(const float* logits, int T, int E, int k, const ScoreRule& rule, const RoutingPtrs& r,
-                          void* ws, hipStream_t s, const TileList& tl, const ActQuant<XT>& aq) {
+                          void* ws, hipStream_t s, const Fp8ItemList& tl, const ActQuant<XT>& aq) {
     const int v = topk_vpl(E);
     if (v == 4) return route_scored_v<4, XT>(logits, T, E, k, rule, r, ws, s, tl, aq);
     if (v == 8) return route_scored_v<8, XT>(logits, T, E, k, rule, r, ws, s, tl, aq);
@@ -558,12 +607,13 @@ hipError_t route_scored_x(const float* logits, int T, int E, int k, const ScoreR
 
 hipError_t launch_route_scored(const float* logits, int T, int E, int k, const ScoreRule& rule, const RoutingPtrs& r,
                                void* ws, hipStream_t s) {
-    return route_scored_x<float>(logits, T, E, k, rule, r, ws, s, TileList{}, ActQuant<float>{});
+    return route_scored_x<float>(logits, T, E, k, rule, r, ws, s, Fp8ItemList{}, ActQuant<float>{});
 }
 
 hipError_t launch_route_quantize_fp8(const float* logits, int T, int E, int k, const ScoreRule& rule,
-                                     const RoutingPtrs& r, void* ws, const TileList& tl, const void* x, ElemType xt, int H,
-                                     uint8_t* xq, float* xs, hipStream_t s) {
+                                     const RoutingPtrs& r, void* ws, const Fp8ItemList& tl, const void* x, ElemType xt,
+                                     int H, uint8_t* xq, float* xs, hipStream_t s, bool* list_done) {
+    *list_done = tl.mt > 0 && (T * k <= kSmallPairs || T <= kPlaceMaxT);
     if (xt == ElemType::kF32)
         return route_scored_x(logits, T, E, k, rule, r, ws, s, tl, ActQuant<float>(x, H, T, H, xq, xs));
     if (xt == ElemType::kF16)
