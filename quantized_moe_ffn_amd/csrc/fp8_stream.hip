@@ -214,8 +214,11 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
     const unsigned char* lb1 = lds + C::NR * 128 + tok(0) * 128 + c1;
     const unsigned char* lsx = lds + C::kRing + tok(0) * 16;
     v4f_f8 acc[WN][WM] = {};
+    int here = 0;   // blocks from s on whose copies were waited for before an epilogue's stores
     for (int s = 0; s < total; ++s) {
-        if (s + STAGES - 2 < total)
+        if (here > 0)
+            --here;
+        else if (s + STAGES - 2 < total)
             wait_vm<(STAGES - 2) * C::kLoads>();
         else
             wait_vm<0>();
@@ -274,6 +277,8 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
                 mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, kWave));
                 if (g == 0) s_amax[wn][tok(j)] = mx;
             }
+            wait_vm<0>();
+            here = STAGES - 1;
             lds_barrier();
             const int64_t row0 = ci.row0;
 #pragma unroll
@@ -298,6 +303,8 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
             const int* pr = reinterpret_cast<const int*>(lds + C::kRing + 2 * C::kXs + cbuf * C::kMeta);
             void* base = ci.shared ? a.y_shared : a.y_pair;
             float* scale = a.y_scale + (ci.shared ? (int64_t)P * (a.N / kPairBlock) : 0);
+            wait_vm<0>();
+            here = STAGES - 1;
 #pragma unroll
             for (int j = 0; j < WM; ++j) {
                 const int m = tok(j);
