@@ -53,7 +53,7 @@ struct Fp8TileArgs {
     void* y;
     ElemType yt;
     int64_t ldy;
-    int vec_ok;                // 4-value stores are aligned
+    int vec_ok;                // 16-byte stores of eight values are aligned
     int n_mt;                  // token tiles
     // grouped
     const int32_t* pair;
@@ -67,35 +67,46 @@ struct Fp8TileArgs {
     int nblocks;               // row blocks
 };
 
-__device__ __forceinline__ void store4(void* base, int64_t idx, ElemType t, const float (&v)[4], int n_ok, bool vec) {
+// Eight neighbouring values of an output row, n_ok of them inside it; vec: 16-byte stores are aligned.
+__device__ __forceinline__ void store8(void* base, int64_t idx, ElemType t, const float (&v)[8], int n_ok, bool vec) {
     if (t == ElemType::kF32) {
         float* p = (float*)base + idx;
-        if (vec && n_ok >= 4) {
+        if (vec && n_ok >= 8) {
             *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i)
                 if (i < n_ok) p[i] = v[i];
         }
         return;
     }
-    uint16_t h[4];
+    uint32_t h[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
         h[i] = t == ElemType::kF16 ? __builtin_bit_cast(uint16_t, (_Float16)v[i])
                                    : __builtin_bit_cast(uint16_t, (__bf16)v[i]);
     uint16_t* p = (uint16_t*)base + idx;
-    if (vec && n_ok >= 4) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+    if (vec && n_ok >= 8) {
+        *reinterpret_cast<uint4*>(p) =
+            make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n_ok) p[i] = h[i];
+        for (int i = 0; i < 8; ++i)
+            if (i < n_ok) p[i] = (uint16_t)h[i];
     }
 }
 
+// The weight row (of a wave's) that row r of its MFMA tiles multiplies: two neighbouring tiles interleave
+// their rows by fours, so that a lane's results, rows 4*g .. 4*g + 3 of both tiles, are eight neighbouring
+// columns of an output row: value v of tile i is column pair_col(i, g) + v.
+__host__ __device__ constexpr int pair_row(int r) {
+    return (r & ~31) + 8 * ((r & 15) >> 2) + 4 * ((r >> 4) & 1) + (r & 3);
+}
+__host__ __device__ constexpr int pair_col(int i, int g) { return 32 * (i >> 1) + 8 * g + 4 * (i & 1); }
+
 // A wave's 64 columns (from n0, one kPairBlock) of an output row: lane group g of the row's four lanes holds
-// columns 16*i + 4*g + v.  Every lane calls it; row < 0: not stored.
+// columns pair_col(i, g) + v.  Every lane calls it; row < 0: not stored.
 template <int WN>
 __device__ __forceinline__ void store_row64(const v4f_f8 (&y)[WN], void* base, float* scale, int pair16, int64_t row, int n0,
                                             int N) {
@@ -103,9 +114,9 @@ __device__ __forceinline__ void store_row64(const v4f_f8 (&y)[WN], void* base, f
     const int g = (threadIdx.x & (kWave - 1)) >> 4;
     if (!pair16) {
         if (row < 0 || n0 >= N) return;
-        float* p = (float*)base + row * N + n0 + 4 * g;
+        float* p = (float*)base + row * N + n0;
 #pragma unroll
-        for (int i = 0; i < WN; ++i) *reinterpret_cast<v4f_f8*>(p + 16 * i) = y[i];
+        for (int i = 0; i < WN; ++i) *reinterpret_cast<v4f_f8*>(p + pair_col(i, g)) = y[i];
         return;
     }
     uint32_t m = 0;
@@ -118,13 +129,15 @@ __device__ __forceinline__ void store_row64(const v4f_f8 (&y)[WN], void* base, f
     if (row < 0 || n0 >= N) return;
     // |y| * 2^-e in [1, 2) at the largest; a block with an infinity or NaN keeps them, and its finite values in range
     const int e = m >= 0x7F800000u ? 113 : (m == 0 ? 0 : __builtin_amdgcn_frexp_expf(__uint_as_float(m)) - 1);
-    uint16_t* p = (uint16_t*)base + row * N + n0 + 4 * g;
+    uint16_t* p = (uint16_t*)base + row * N + n0;
 #pragma unroll
-    for (int i = 0; i < WN; ++i) {
-        uint32_t h[4];
+    for (int i = 0; i < WN; i += 2) {
+        uint32_t h[8];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) h[v] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_ldexpf(y[i][v], -e));
-        *reinterpret_cast<uint2*>(p + 16 * i) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+        for (int v = 0; v < 8; ++v)
+            h[v] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_ldexpf(y[i + (v >> 2)][v & 3], -e));
+        *reinterpret_cast<uint4*>(p + pair_col(i, g)) =
+            make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
     }
     if (g == 0) scale[row * (N / kPairBlock) + n0 / kPairBlock] = __builtin_ldexpf(1.0f, e);
 }
@@ -224,15 +237,15 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
     for (int i = 0; i < C::NA; ++i) {
         const int R8 = (wave + i * C::kWaves) * 8;   // the copy's first row in the tile
         if constexpr (MODE == kFp8GateUp) {
-            const int w_ = R8 / (WN * 16), t_ = (R8 / 16) % WN, r_ = R8 & 15;
-            const int row = nb * (C::NR / 2) + w_ * (WN / 2 * 16) + (t_ % (WN / 2)) * 16 + r_;
-            const Fp8Mat& m = t_ < WN / 2 ? m0 : m1;
+            const int w_ = R8 / (WN * 16), r_ = R8 % (WN * 16);
+            const int row = nb * (C::NR / 2) + w_ * (WN / 2 * 16) + pair_row(r_ % (WN / 2 * 16));
+            const Fp8Mat& m = r_ < WN / 2 * 16 ? m0 : m1;
             ba[i] = wave_uniform((uint64_t)(m.data + (int64_t)row * m.row_stride));
-            oa[i] = (uint32_t)(lr * (int)m.row_stride + ca);
+            oa[i] = (uint32_t)(pair_row(lr) * (int)m.row_stride + ca);
         } else {
             const int first = min(nb * C::NR, a.N - 1);
             ba[i] = wave_uniform((uint64_t)(m0.data + (int64_t)first * m0.row_stride));
-            oa[i] = (uint32_t)((min(nb * C::NR + R8 + lr, a.N - 1) - first) * (int)m0.row_stride + ca);
+            oa[i] = (uint32_t)((min(nb * C::NR + pair_row(R8 + lr), a.N - 1) - first) * (int)m0.row_stride + ca);
         }
     }
     const int64_t tok0 = MODE == kFp8Dense ? mt0 : (MODE == kFp8Down ? off : 0);
@@ -463,17 +476,18 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
         if (grp == 0) meet();
     }
 
-    // value v of acc[i][j]: weight row 16*i + 4*g + v of the wave, token 16*j + r16 of the wave
+    // value v of acc[i][j]: weight row pair_col(i, g) + v of the wave, token 16*j + r16 of the wave
     if constexpr (MODE == kFp8Dense) {
 #pragma unroll
         for (int j = 0; j < WM; ++j) {
             const int m = (wm * WM + j) * 16 + r16;
             if (m >= n_tok) continue;
 #pragma unroll
-            for (int i = 0; i < WN; ++i) {
-                const int n = nb * C::NR + (wn * WN + i) * 16 + 4 * g;
-                const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                if (n < a.N) store4(a.y, (int64_t)(mt0 + m) * a.ldy + n, a.yt, v, a.N - n, a.vec_ok);
+            for (int i = 0; i < WN; i += 2) {
+                const int n = nb * C::NR + wn * WN * 16 + pair_col(i, g);
+                const float v[8] = {acc[i][j][0],     acc[i][j][1],     acc[i][j][2],     acc[i][j][3],
+                                    acc[i + 1][j][0], acc[i + 1][j][1], acc[i + 1][j][2], acc[i + 1][j][3]};
+                if (n < a.N) store8(a.y, (int64_t)(mt0 + m) * a.ldy + n, a.yt, v, a.N - n, a.vec_ok);
             }
         }
     } else if constexpr (MODE == kFp8Down) {
@@ -517,10 +531,12 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_tile_kernel(const Fp8Tile
             if (!fin) raise_error(kErrActNonFinite);
             const Fp8Rule rule(__uint_as_float(fin ? mx : 0u));
 #pragma unroll
-            for (int i = 0; i < HI; ++i) {
-                const uint32_t q = fin ? rule.pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]) : 0u;
-                const int col = nb * (C::NR / 2) + (wn * HI + i) * 16 + 4 * g;
-                *reinterpret_cast<uint32_t*>(a.hq + (row0 + m) * a.N + col) = q;
+            for (int i = 0; i < HI; i += 2) {
+                const uint32_t q0 = fin ? rule.pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]) : 0u;
+                const uint32_t q1 =
+                    fin ? rule.pack4(acc[i + 1][j][0], acc[i + 1][j][1], acc[i + 1][j][2], acc[i + 1][j][3]) : 0u;
+                const int col = nb * (C::NR / 2) + wn * HI * 16 + pair_col(i, g);
+                *reinterpret_cast<uint2*>(a.hq + (row0 + m) * a.N + col) = make_uint2(q0, q1);
             }
             if (wn == 0 && g == 0) a.hs[(row0 + m) * (a.N / kFp8Block) + nb] = rule.d;
         }
@@ -661,7 +677,7 @@ hipError_t launch_matmul_fp8(const Fp8MatmulArgs& m, hipStream_t s) {
     a.yt = m.yt;
     a.ldy = m.ldy;
     const int sz = m.yt == ElemType::kF32 ? 4 : 2;
-    a.vec_ok = m.ldy % 4 == 0 && (uintptr_t)m.y % (4 * sz) == 0;
+    a.vec_ok = m.ldy * sz % 16 == 0 && (uintptr_t)m.y % 16 == 0;
     const bool exact = m.yt == ElemType::kF32;
     // the largest tile that gives the chip's 256 CUs work: 64 x 64, 256 x 128 or 256 x 256 (rows x tokens)
     const int64_t big = (m.w.rows + 255) / 256;
@@ -722,9 +738,7 @@ __global__ void __launch_bounds__(256) combine_fp8_kernel(const Fp8CombineArgs a
 #pragma unroll
         for (int q = 0; q < 8; ++q) acc[q] = fmaf(w, v[q], acc[q]);
     }
-    const float lo[4] = {acc[0], acc[1], acc[2], acc[3]}, hi[4] = {acc[4], acc[5], acc[6], acc[7]};
-    store4(a.out, t * a.H + o, a.ot, lo, 4, true);
-    store4(a.out, t * a.H + o + 4, a.ot, hi, 4, true);
+    store8(a.out, t * a.H + o, a.ot, acc, 8, true);
 }
 
 }  // namespace

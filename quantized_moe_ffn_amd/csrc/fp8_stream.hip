@@ -114,15 +114,15 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
         for (int i = 0; i < C::NA; ++i) {
             const int R8 = (wave + i * C::kWaves) * 8;
             if constexpr (kGu) {
-                const int w_ = R8 / (WN * 16), t_ = (R8 / 16) % WN, r_ = R8 & 15;
-                const int row = it.nb * (C::NR / 2) + w_ * (WN / 2 * 16) + (t_ % (WN / 2)) * 16 + r_;
-                const bool up = t_ >= WN / 2;
+                const int w_ = R8 / (WN * 16), r_ = R8 % (WN * 16);
+                const int row = it.nb * (C::NR / 2) + w_ * (WN / 2 * 16) + pair_row(r_ % (WN / 2 * 16));
+                const bool up = r_ >= WN / 2 * 16;
                 ba[i] = wave_uniform((uint64_t)(up ? d1 : d0) + (uint64_t)row * (uint32_t)(up ? r1 : r0));
-                oa[i] = (uint32_t)(lr * (up ? r1 : r0) + ca);
+                oa[i] = (uint32_t)(pair_row(lr) * (up ? r1 : r0) + ca);
             } else {
                 const int row0 = it.nb * C::NR;
                 ba[i] = wave_uniform((uint64_t)d0 + (uint64_t)row0 * (uint32_t)r0);
-                oa[i] = (uint32_t)((min(row0 + R8 + lr, a.N - 1) - row0) * r0 + ca);
+                oa[i] = (uint32_t)((min(row0 + pair_row(R8 + lr), a.N - 1) - row0) * r0 + ca);
             }
         }
         // token operand: gate/up gathers rows of x, down reads the bucket's rows of h
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
         if ((kb & 3) == 3) xs ^= C::kXs;
         if (++kb < KB) continue;
 
-        // The item's results: value v of acc[i][j] is weight row 16*i + 4*g + v of the wave, token tok(j).
+        // The item's results: value v of acc[i][j] is weight row pair_col(i, g) + v of the wave, token tok(j).
         // The copies of the next item's first blocks are in flight.
         if constexpr (kGu) {
             constexpr int HI = WN / 2;
@@ -292,10 +292,12 @@ __global__ void __launch_bounds__(NWN* NWM* kWave) fp8_stream_kernel(const Fp8Ti
                 if (!fin) raise_error(kErrActNonFinite);
                 const Fp8Rule rule(__uint_as_float(fin ? mx : 0u));
 #pragma unroll
-                for (int i = 0; i < HI; ++i) {
-                    const uint32_t q = fin ? rule.pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]) : 0u;
-                    const int col = ci.nb * (C::NR / 2) + (wn * HI + i) * 16 + 4 * g;
-                    *reinterpret_cast<uint32_t*>(a.hq + (row0 + m) * a.N + col) = q;
+                for (int i = 0; i < HI; i += 2) {
+                    const uint32_t q0 = fin ? rule.pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]) : 0u;
+                    const uint32_t q1 =
+                        fin ? rule.pack4(acc[i + 1][j][0], acc[i + 1][j][1], acc[i + 1][j][2], acc[i + 1][j][3]) : 0u;
+                    const int col = ci.nb * (C::NR / 2) + wn * HI * 16 + pair_col(i, g);
+                    *reinterpret_cast<uint2*>(a.hq + (row0 + m) * a.N + col) = make_uint2(q0, q1);
                 }
                 if (wn == 0 && g == 0) a.hs[(row0 + m) * (a.N / kFp8Block) + ci.nb] = rule.d;
             }
