@@ -587,10 +587,13 @@ int fp8_max_tiles(int T, int k, int E, int has_shared, int mt) {
     return (int)(P / mt + act + (has_shared ? (T + mt - 1) / mt : 0));
 }
 
+// Four token scales of a row in one 16-byte copy: K in whole groups of four blocks, rows 16-byte aligned.
+bool wide_scales(const Fp8TileArgs& a) { return a.K % (4 * kFp8Block) == 0 && (uintptr_t)a.xs % 16 == 0; }
+
 // Persistent workgroups where the shape allows; else the tiles, with fp32 sums.
 template <int MODE, bool EXACT>
 hipError_t launch_grouped(const Fp8TileArgs& a, int64_t n_work, hipStream_t s) {
-    if (fp8_stream_k(a.K)) {
+    if (wide_scales(a) && a.K <= kStreamMaxK) {
         if (a.tl.mt == 32) return launch_stream<MODE, EXACT, 4, 1, 4, 2, 2>(a, n_work, s);
         if (a.tl.mt == 64) return launch_stream<MODE, EXACT, 4, 2, 4, 2, 3>(a, n_work, s);
         return launch_stream<MODE, EXACT, 4, 2, 4, 4, 3>(a, n_work, s);
@@ -603,7 +606,7 @@ hipError_t launch_grouped(const Fp8TileArgs& a, int64_t n_work, hipStream_t s) {
 template <bool EXACT>
 hipError_t launch_dense(const Fp8TileArgs& a, int mt, int64_t n_work, hipStream_t s) {
     if (mt == 64) return launch_tile<kFp8Dense, EXACT, false, 2, 2, 2, 2, 4>(a, n_work, s);
-    if (mt == 128 && a.K % (4 * kFp8Block)) return launch_tile<kFp8Dense, EXACT, false, 4, 2, 4, 4, 3>(a, n_work, s);
+    if (mt == 128 && !wide_scales(a)) return launch_tile<kFp8Dense, EXACT, false, 4, 2, 4, 4, 3>(a, n_work, s);
     if (mt == 128) return launch_tile<kFp8Dense, EXACT, true, 4, 2, 4, 4, 3>(a, n_work, s);
     return launch_tile<kFp8Dense, false, true, 4, 2, 4, 8, 2>(a, n_work, s);
 }
@@ -681,7 +684,7 @@ hipError_t launch_matmul_fp8(const Fp8MatmulArgs& m, hipStream_t s) {
     const bool exact = m.yt == ElemType::kF32;
     // the largest tile that gives the chip's 256 CUs work: 64 x 64, 256 x 128 or 256 x 256 (rows x tokens)
     const int64_t big = (m.w.rows + 255) / 256;
-    const int mt = big * ((m.T + 127) / 128) < 128 ? 64 : (exact || m.w.cols % (4 * kFp8Block) || big * ((m.T + 255) / 256) < 128 ? 128 : 256);
+    const int mt = big * ((m.T + 127) / 128) < 128 ? 64 : (exact || !wide_scales(a) || big * ((m.T + 255) / 256) < 128 ? 128 : 256);
     a.nblocks = mt == 64 ? (m.w.rows + 63) / 64 : (int)big;
     a.n_mt = (m.T + mt - 1) / mt;
     const int64_t n_work = (int64_t)a.nblocks * a.n_mt;

@@ -184,6 +184,40 @@ def test_matmul_integers_are_exact(T):
     assert np.array_equal(y.cpu().numpy().astype(np.float64), r)
 
 
+@pytest.mark.parametrize("yt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,N,K,odd_xs", [(2100, 2060, 512, False),     # tiles of 256 x 128
+                                          (2100, 2060, 640, False), (2100, 2060, 512, True),   # the same without groups of four blocks
+                                          (2900, 2900, 1024, False),    # 256 x 256 for 16-bit outputs
+                                          (1050, 8192 - 3, 8704, False)])   # more than 64 blocks
+def test_matmul_many_rows(T, N, K, odd_xs, yt):
+    """Large tiles: small integers, whose sums are exact, in all places; drawn values against 64 bits at sampled rows."""
+    m = _qm()
+    print("matmul", T, N, K, odd_xs, yt, flush=True)
+    g = np.random.default_rng(T + N + K)
+    xv, wv = (torch.from_numpy(g.integers(-1, 2, n).astype(np.float32)).to(DEV) for n in ((T, K), (N, K)))
+    xs = torch.empty(T * ref.nb(K) + 1, device=DEV)[int(odd_xs):][:T * ref.nb(K)].view(T, ref.nb(K)).fill_(1.0)
+    ws = np.full((1, ref.nb(N), ref.nb(K)), 0.5, np.float32)
+    big = torch.full((T + 1, N + 5), -7.0, dtype=DT[yt], device=DEV)
+    table = torch.from_numpy(ref.encode(np.array([-1.0, 0.0, 1.0]))).to(DEV)
+    def codes(v):
+        return table[(v + 1).long()]
+    m.moe_matmul_fp8(codes(xv), xs, m.Fp8Matrix(codes(wv)[None], torch.from_numpy(ws).to(DEV)), big[:T, :N])
+    want = (xv @ wv.T) * 0.5    # fp32 holds every partial sum
+    assert torch.equal(big[:T, :N], want.to(DT[yt]))
+    assert (big[T] == -7).all() and (big[:, N:] == -7).all()
+    q, d = _quantize(m, torch.from_numpy(g.standard_normal((T, K)).astype(np.float32)).to(DEV))
+    xs.copy_(d)
+    wq, s = _weights(g, 1, N, K)
+    y = torch.empty(T, N, dtype=DT[yt], device=DEV)
+    m.moe_matmul_fp8(q, xs, _matrix(m, wq, s), y)
+    m.moe_check_device_errors()
+    at = np.unique(np.concatenate([[0, T - 1], g.integers(0, T, 30)]))
+    r, bound = ref.matmul(_codes(q)[at], d.cpu().numpy()[at], wq[0], s[0], fast=yt != "f32")
+    half = 0 if yt == "f32" else torch.finfo(DT[yt]).eps / 2
+    got = y.double().cpu().numpy()[at]
+    assert (np.abs(got - r) <= bound * (1 + half) + np.abs(r) * half + (2.0 ** -25 if yt == "f16" else 0)).all()
+
+
 def test_matmul_strided_weights():
     m = _qm()
     g = np.random.default_rng(4)
@@ -234,6 +268,31 @@ def _reference(host, xq, xs, idx, fast=False):
     if "sh_gate" not in host:
         return y, dy, None, None
     return (y, dy) + ref.expert(xq, xs, *((host["sh_" + n][0][0], host["sh_" + n][1][0]) for n in ("gate", "up", "down")), fast=fast)
+
+
+def _expected(host, xq, xs, idx, w, sc, xt, flags):
+    """The layer's output rows for the given tokens, and the limit of their error."""
+    T, k = idx.shape
+    H = xq.shape[1]
+    y, dy, sh, dsh = _reference(host, xq, xs, idx, fast=xt == "bf16")
+    def handed(v, dv):   # the 16-bit hand-off: fp16 times a power of two below twice the block's largest
+        if not flags:
+            return dv
+        big = np.repeat((np.abs(v) + dv).reshape(len(v), -1, 64).max(axis=2), 64, 1)
+        return dv + 2.0 ** -11 * (np.abs(v) + dv) + 2.0 ** -25 * big
+    dy = handed(y, dy)
+    a = np.abs(w)[:, :, None]
+    o = (w[:, :, None] * y.reshape(T, k, H)).sum(1)
+    mag = (a * np.abs(y).reshape(T, k, H)).sum(1)
+    do = (a * dy.reshape(T, k, H)).sum(1)
+    if sh is not None:
+        s = sc.double().cpu().numpy()[:, None]
+        o = o + s * sh
+        do += s * handed(sh, dsh)
+        mag += s * np.abs(sh)
+    do += (k + 3) * ref.U * (mag + do)                             # fp32 weights, k + 1 fmas
+    half = 0 if xt == "f32" else torch.finfo(DT[xt]).eps / 2
+    return o, do * (1 + half) + np.abs(o) * half + (2.0 ** -25 if xt == "f16" else 0)
 
 
 LAYERS = [  # T, E, k, H, I, shared
@@ -290,28 +349,73 @@ def test_forward(T, E, k, H, I, shared, xt, flags):
     idx, w = ref.route(lg, k, bias=bias, **kw)
     assert np.array_equal(r.idx.cpu().numpy(), idx)
     q, d = _quantize(m, x)
-    y, dy, sh, dsh = _reference(host, _codes(q), d.cpu().numpy(), idx, fast=xt == "bf16")
-    def handed(v, dv):   # the 16-bit hand-off: fp16 times a power of two below twice the block's largest
-        if not flags:
-            return dv
-        big = np.repeat((np.abs(v) + dv).reshape(len(v), -1, 64).max(axis=2), 64, 1)
-        return dv + 2.0 ** -11 * (np.abs(v) + dv) + 2.0 ** -25 * big
-    dy = handed(y, dy)
-    a = np.abs(w)[:, :, None]
-    o = (w[:, :, None] * y.reshape(T, k, H)).sum(1)
-    mag = (a * np.abs(y).reshape(T, k, H)).sum(1)
-    do = (a * dy.reshape(T, k, H)).sum(1)
-    if shared:
-        s = sc.double().cpu().numpy()[:, None]
-        o = o + s * sh
-        do += s * handed(sh, dsh)
-        mag += s * np.abs(sh)
-    do += (k + 3) * ref.U * (mag + do)                             # fp32 weights, k + 1 fmas
-    half = 0 if xt == "f32" else torch.finfo(DT[xt]).eps / 2
+    o, lim = _expected(host, _codes(q), d.cpu().numpy(), idx, w, sc, xt, flags)
     got = out.double().cpu().numpy()
-    lim = do * (1 + half) + np.abs(o) * half + (2.0 ** -25 if xt == "f16" else 0)
     assert (np.abs(got[:-1] - o) <= lim).all(), (np.abs(got[:-1] - o) / lim).max()
     assert (got[-1] == -3).all()
+
+
+@pytest.mark.parametrize("xt,flags", [("f32", 0), ("bf16", 16)])
+@pytest.mark.parametrize("T,E,k,H,I,shared", [
+    (2600, 8, 4, 2048, 1024, True),      # tiles of 128 tokens, several items a workgroup in both products
+    (900, 64, 4, 1024, 512, True),       # of 64
+    (1280, 40, 1, 512, 2048, False),     # of 32
+    (1111, 2, 2, 1024, 1024, True),      # two long buckets
+    (100, 2, 1, 8704, 128, False),       # rows longer than 64 scale blocks
+    (17000, 4, 2, 512, 128, True),       # more tokens than one placing pass
+    (70, 1024, 2, 512, 512, False),      # most experts without a token
+])
+def test_forward_long(T, E, k, H, I, shared, xt, flags):
+    """Long calls against the reference at sampled tokens, with a hot expert and experts without a token."""
+    m = _qm()
+    print("forward long", xt, flags, T, E, k, H, I, shared, flush=True)
+    g = np.random.default_rng(T + E + I)
+    L, host = _layer(m, g, E, H, I, shared)
+    lg = g.standard_normal((T, E)).astype(np.float32)
+    lg[: T // 3, E // 2] += 4
+    x = torch.from_numpy(g.standard_normal((T, H)).astype(np.float32)).to(DT[xt]).to(DEV)
+    sc = torch.from_numpy(g.uniform(0.5, 1.5, T).astype(np.float32)).to(DEV) if shared else None
+    out = torch.full((T + 1, H), -3.0, dtype=DT[xt], device=DEV)
+    r = m.Routing(T, E, k, DEV)
+    ws = torch.full((m.moe_forward_fp8_workspace_bytes(L, T, k, flags),), 0x7F, dtype=torch.uint8, device=DEV)
+    m.moe_forward_fp8(L, torch.from_numpy(lg).to(DEV), x, k, r, m.RouteSpec(), out[:T], sc, flags, ws)
+    m.moe_check_device_errors()
+    at = np.unique(np.concatenate([[0, 1, T // 3 - 1, T // 3, T - 2, T - 1], g.integers(0, T, 40)]))
+    idx, w = ref.route(lg[at], k)
+    assert np.array_equal(r.idx.cpu().numpy()[at], idx)
+    q, d = _quantize(m, x)
+    o, lim = _expected(host, _codes(q)[at], d.cpu().numpy()[at], idx, w, sc[torch.from_numpy(at).to(DEV)] if shared else None, xt, flags)
+    got = out.double().cpu().numpy()
+    assert (np.abs(got[at] - o) <= lim).all(), (np.abs(got[at] - o) / lim).max()
+    assert (got[-1] == -3).all() and np.isfinite(got).all()
+    # every token: the same call once more, its tokens in reverse
+    out2 = torch.empty_like(x)
+    m.moe_forward_fp8(L, torch.from_numpy(lg[::-1].copy()).to(DEV), x.flip(0).contiguous(), k, r, m.RouteSpec(), out2,
+                      sc.flip(0).contiguous() if shared else None, flags, ws)
+    assert torch.equal(out2.flip(0), out[:T])
+
+
+@pytest.mark.parametrize("T,H", [(40, 512), (300, 512), (300, 1024)])
+def test_unaligned_token_scales(T, H):
+    """xs needs 4-byte alignment only; the results are those of an aligned one, bit for bit in fp32."""
+    m = _qm()
+    g = np.random.default_rng(T)
+    E, k, I = 4, 2, 512
+    L, _ = _layer(m, g, E, H, I, True)
+    r = m.Routing(T, E, k, DEV)
+    m.moe_route_scored(torch.randn(T, E, device=DEV), k, r, m.RouteSpec(),
+                       torch.empty(max(4, m.moe_route_workspace_bytes(T, E, k)), dtype=torch.uint8, device=DEV))
+    q, d = _quantize(m, torch.randn(T, H, device=DEV))
+    odd = torch.empty(d.numel() + 1, device=DEV)[1:].view(d.shape)
+    odd.copy_(d)
+    ws = torch.empty(m.moe_ffn_fp8_workspace_bytes(L, T, k), dtype=torch.uint8, device=DEV)
+    res = []
+    for s in (d, odd):
+        yp, ys = torch.empty(T * k, H, device=DEV), torch.empty(T, H, device=DEV)
+        m.moe_expert_ffn_fp8(L, r, T, k, yp, q, s, ys, ws)
+        res += [yp, ys]
+    m.moe_check_device_errors()
+    assert torch.equal(res[0], res[2]) and torch.equal(res[1], res[3])
 
 
 def test_forward_is_its_stages_and_repeats_bitwise():
@@ -356,18 +460,20 @@ def test_a_token_does_not_depend_on_its_neighbours():
     assert torch.equal(out[p], out2)
 
 
-def test_foreign_routing_buffers_raise_without_a_fault():
+@pytest.mark.parametrize("T,H,I", [(40, 256, 128), (40, 512, 512), (600, 512, 512)])
+def test_foreign_routing_buffers_raise_without_a_fault(T, H, I):
     """Counts, offsets and pair ids outside their range set the error word; nothing out of bounds is touched."""
     m = _qm()
     g = np.random.default_rng(2)
-    T, E, k, H, I = 40, 4, 2, 256, 128
+    E, k = 4, 2
     L, _ = _layer(m, g, E, H, I, False)
     q, d = _quantize(m, torch.randn(T, H, device=DEV))
     ws = torch.empty(m.moe_ffn_fp8_workspace_bytes(L, T, k), dtype=torch.uint8, device=DEV)
     yp = torch.zeros(T * k, H, device=DEV)
     for spoil in ("pair", "count", "offset"):
         r = m.Routing(T, E, k, DEV)
-        m.moe_route_scored(torch.randn(T, E, device=DEV), k, r, m.RouteSpec())
+        m.moe_route_scored(torch.randn(T, E, device=DEV), k, r, m.RouteSpec(),
+                           torch.empty(max(4, m.moe_route_workspace_bytes(T, E, k)), dtype=torch.uint8, device=DEV))
         t = getattr(r, spoil)
         t[1] = 1 << 20
         m.moe_expert_ffn_fp8(L, r, T, k, yp, q, d, workspace=ws)
