@@ -576,9 +576,12 @@ hipError_t launch_tile(const Fp8TileArgs& a, int64_t n_work, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Tokens per tile by the mean bucket.  Layer of 256 experts / top-8, H 2048, I 512, us with tiles of 32 / 64 / 128:
+// bf16, 0.5 tokens an expert 74 / 79 / 83, 2: 123 / 116 / 123, 4: 133 / 129 / 135, 8: 147 / 154 / 162,
+// 47: 234 / 219 / 222, 64: 269 / 238 / 230, 128: 403 / 324 / 305; fp16, 16: 190 / 182 / 200, 64: 308 / 296 / 310.
 int fp8_tile_tokens(int T, int k, int E) {
     const int64_t per = ((int64_t)T * k + E - 1) / E;
-    return per <= 32 ? 32 : (per <= 64 ? 64 : 128);
+    return per <= 1 ? 32 : (per <= 64 ? 64 : 128);
 }
 
 int fp8_max_tiles(int T, int k, int E, int has_shared, int mt) {
@@ -668,7 +671,10 @@ hipError_t launch_ffn_fp8(const Fp8FfnArgs& f, bool list_done, hipStream_t s) {
 }
 
 hipError_t launch_matmul_fp8(const Fp8MatmulArgs& m, hipStream_t s) {
-    if (m.T <= 32) return launch_skinny_matmul(m, s);
+    // The split-K product up to 32 tokens, unless the tiles of 64 x 64 fill the chip and a second token tile makes
+    // it slower: K 2048, us with it / with the tiles: 16 tokens, 16,384 rows 9.0 / 11.9; 32 tokens, 8,192 rows
+    // 8.7 / 11.1, 16,384 rows 15.7 / 12.3.
+    if (m.T <= 16 || (m.T <= 32 && m.w.rows <= 12288)) return launch_skinny_matmul(m, s);
     Fp8TileArgs a{};
     a.w0 = m.w;
     a.xq = m.xq;
@@ -682,9 +688,14 @@ hipError_t launch_matmul_fp8(const Fp8MatmulArgs& m, hipStream_t s) {
     const int sz = m.yt == ElemType::kF32 ? 4 : 2;
     a.vec_ok = m.ldy * sz % 16 == 0 && (uintptr_t)m.y % 16 == 0;
     const bool exact = m.yt == ElemType::kF32;
-    // the largest tile that gives the chip's 256 CUs work: 64 x 64, 256 x 128 or 256 x 256 (rows x tokens)
+    // 64 x 64 tiles, 256 x 128 or 256 x 256 (rows x tokens).  Measured at K 4096, us: 4096 rows of bf16,
+    // 768 tokens 39 / 33 / -, 1,024: 42 / 34 / 62, 2,048: 78 / 38 / 64, 3,000: - / 67 / 65, 4,096: 150 / 76 / 71;
+    // 512 x 2048: 20 / 32 / 62; fp32, 768 tokens 44 / 69, 1,024: 53 / 69.  So one round of 256 x 128 tiles on the 256
+    // CUs pays from 96 of them (fp32 sums: 192) on, and a round of 256 x 256 ones costs 1.85 of theirs.
     const int64_t big = (m.w.rows + 255) / 256;
-    const int mt = big * ((m.T + 127) / 128) < 128 ? 64 : (exact || !wide_scales(a) || big * ((m.T + 255) / 256) < 128 ? 128 : 256);
+    const int64_t n128 = big * ((m.T + 127) / 128), n256 = big * ((m.T + 255) / 256);
+    const bool wide = !exact && wide_scales(a) && 1.85 * ((n256 + kCus - 1) / kCus) < (double)((n128 + kCus - 1) / kCus);
+    const int mt = n128 < (exact ? 192 : 96) ? 64 : (wide ? 256 : 128);
     a.nblocks = mt == 64 ? (m.w.rows + 63) / 64 : (int)big;
     a.n_mt = (m.T + mt - 1) / mt;
     const int64_t n_work = (int64_t)a.nblocks * a.n_mt;

@@ -188,6 +188,7 @@ def test_matmul_integers_are_exact(T):
 @pytest.mark.parametrize("T,N,K,odd_xs", [(2100, 2060, 512, False),     # tiles of 256 x 128
                                           (2100, 2060, 640, False), (2100, 2060, 512, True),   # the same without groups of four blocks
                                           (2900, 2900, 1024, False),    # 256 x 256 for 16-bit outputs
+                                          (2900, 2900, 640, False), (20, 12300, 512, False),
                                           (1050, 8192 - 3, 8704, False)])   # more than 64 blocks
 def test_matmul_many_rows(T, N, K, odd_xs, yt):
     """Large tiles: small integers, whose sums are exact, in all places; drawn values against 64 bits at sampled rows."""
