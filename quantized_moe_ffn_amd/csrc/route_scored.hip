@@ -16,6 +16,8 @@
 // One wave per token, lane l holding experts l, l + 64, ...: a logit row is
 // read once, coalesced.  Bound: latency (one token) or the fp64 exponentials
 // and k extraction rounds (a prompt chunk; the logits are 4 MB, ~1 us of HBM).
+// Measured: one token of 256 experts in 8 groups 6.1 us a call, 777 tokens of
+// 512 experts / top-10 14.0, 4,096 tokens of 256 experts in 8 groups 15.1.
 //
 // Bucketing uses that a token names an expert at most once: the tokens of a
 // tile that chose e form a bit mask, so a pair's rank within its tile is a
@@ -26,7 +28,9 @@
 //     workgroups each sum the byte counts of all tiles (E bytes a tile, from
 //     L2) and place their tiles' pairs.
 //   * above that the sums every workgroup repeats would grow quadratically:
-//     the tiled counting sort of route.hip (three launches) places the pairs.
+//     the tiled counting sort of route.hip (three launches) places the pairs
+//     (4,096 tokens: 15.1 us with the placing kernel, 22.7 with the sort;
+//     16,384: 44.2 and 53.3).
 #include "fp8.h"
 
 namespace moe {
@@ -578,7 +582,8 @@ hipError_t route_scored_v(const float* logits, int T, int E, int k, const ScoreR
     }
     // 64-token tiles for k < 4 keep the counts within route_workspace_bytes: ceil(T/64) * E bytes there,
     // ceil(T/16) * E <= ceil(T*k/256) * E * 4 for k >= 4
-    // (8-token tiles, for k >= 8, spread a batch of up to 2,048 tokens over twice the CUs)
+    // (8-token tiles, for k >= 8, spread a batch of up to 2,048 tokens over twice the CUs: 777 tokens 11.2 us
+    // against 13.4 with 16, 2,048 12.8 / 13.9, 4,096 17.8 / 15.1)
     const int tt = k < 4 ? 64 : (k >= 8 && T <= 2048 ? 8 : 16);
     const int n_tiles = (T + tt - 1) / tt;
     const int hist_ld = (E + 3) / 4 * 4;
