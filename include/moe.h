@@ -455,7 +455,9 @@ size_t moe_forward_fp8_workspace_bytes(const moe_fp8_layer* L, int32_t T, int32_
  * MOE_FFN_PAIR_BF16 in bf16's size, as fp16 values times one power of two for
  * each 64 columns of a row (each y then moves by at most 2^-11 * |y| + 2^-25 of
  * the largest of its 64 columns); ffn_flags is otherwise 0.  Batches of few
- * pairs combine in the down projection's kernel, without a hand-off. */
+ * pairs combine in the down projection's kernel, without a hand-off.  Calls
+ * that overlap in time, captured ones included, need workspaces and routing
+ * buffers of their own. */
 moe_status moe_forward_fp8(const moe_fp8_layer* L, const moe_route_spec* spec, const float* logits, const void* x,
                            int32_t x_type, int32_t T, int32_t k, uint32_t ffn_flags, const moe_routing* r,
                            const float* shared_scale, void* out, void* workspace, size_t ws_bytes,

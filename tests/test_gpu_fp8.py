@@ -482,6 +482,28 @@ def test_foreign_routing_buffers_raise_without_a_fault(T, H, I):
             m.moe_check_device_errors()
 
 
+def test_foreign_experts_of_few_pairs_raise_without_a_fault():
+    """An expert index outside the layer sets the error word; the other pairs keep their results."""
+    m = _qm()
+    g = np.random.default_rng(3)
+    T, E, k, H, I = 3, 16, 4, 256, 128
+    L, _ = _layer(m, g, E, H, I, True)
+    q, d = _quantize(m, torch.randn(T, H, device=DEV))
+    ws = torch.empty(m.moe_ffn_fp8_workspace_bytes(L, T, k), dtype=torch.uint8, device=DEV)
+    r = m.Routing(T, E, k, DEV)
+    m.moe_route_scored(torch.randn(T, E, device=DEV), k, r, m.RouteSpec())
+    want, ys = torch.empty(T * k, H, device=DEV), torch.empty(T, H, device=DEV)
+    m.moe_expert_ffn_fp8(L, r, T, k, want, q, d, ys, ws)
+    for bad in (E, -1, 1 << 30):
+        r.idx[1, 2] = bad
+        yp, y2 = torch.zeros(T * k, H, device=DEV), torch.empty(T, H, device=DEV)
+        m.moe_expert_ffn_fp8(L, r, T, k, yp, q, d, y2, ws)
+        with pytest.raises(m.MoeError, match="out of range"):
+            m.moe_check_device_errors()
+        keep = [p for p in range(T * k) if p != k + 2]
+        assert torch.equal(yp[keep], want[keep]) and torch.equal(y2, ys)
+
+
 def test_captured_layer_replays():
     """The layer captured in a graph, replayed with new inputs between eager work."""
     m = _qm()
